@@ -62,6 +62,16 @@ _SIGS = {
     "bsq_quant_nvfp4_gather_workspace": (C.c_size_t, [_i64, _i64]),
     "bsq_quant_nvfp4_gather": (C.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, C.c_int, C.c_int, C.c_uint16, C.c_int,
                                          _vp, _vp, _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "bsq_moe_route_workspace": (C.c_size_t, [_i64, _i64]),
+    "bsq_moe_route": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, _vp, C.c_int, C.c_int, _vp, _vp, _vp, _vp, _vp, _vp,
+                                _vp, _vp, C.c_float, _vp, _vp, C.c_size_t, _vp]),
+    "bsq_moe_route_bwd": (C.c_int, [_vp, C.c_int, _i64, _i64, _i64, C.c_int, C.c_int, _vp, _vp, _vp, _vp, C.c_float,
+                                    _vp, _vp, _i64, _vp]),
+    "bsq_moe_combine": (C.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, C.c_int, _vp, _i64, _vp]),
+    "bsq_moe_combine_bwd": (C.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, C.c_int, _vp, _i64,
+                                      _vp, _vp]),
+    "bsq_swiglu_ckpt": (C.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "bsq_swiglu_ckpt_bwd": (C.c_int, [_vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp]),
     "bsq_check": (C.c_int, [_vp]),
     "bsq_debug_timeout_probe": (C.c_int, [C.c_uint64, _vp]),
     "bsq_debug_kernel_choice": (C.c_int, [C.c_int, C.c_int]),
@@ -247,3 +257,45 @@ def bsq_quant_nvfp4_gather(x, T, K, ldx, row_index, M, four_over_six, rht_enable
         _p(x), T, K, ldx, _p(row_index), M, int(four_over_six), int(rht_enable), rht_sign_mask, G, _p(row_offsets),
         _p(sf_row_offsets), _p(amax_in), _p(global_scale), _p(codes), _p(sf), _p(workspace), workspace_bytes,
         _stream(stream)))
+
+
+def bsq_moe_route_workspace(T, E):
+    return int(lib().bsq_moe_route_workspace(T, E))
+
+
+def bsq_moe_route(logits, logits_type, T, E, ldl, token_mask, topk, renorm, expert_ids, weights, rows, row_index,
+                  row_offsets, sf_row_offsets, counts, prob_sums, balance_coef, loss, workspace, workspace_bytes,
+                  stream=None):
+    return _check("bsq_moe_route", lib().bsq_moe_route(
+        _p(logits), logits_type, T, E, ldl, _p(token_mask), topk, int(renorm), _p(expert_ids), _p(weights), _p(rows),
+        _p(row_index), _p(row_offsets), _p(sf_row_offsets), _p(counts), _p(prob_sums), balance_coef, _p(loss),
+        _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def bsq_moe_route_bwd(logits, logits_type, T, E, ldl, topk, renorm, expert_ids, weights, dweights, counts,
+                      balance_coef, dloss, dlogits, ldd, stream=None):
+    return _check("bsq_moe_route_bwd", lib().bsq_moe_route_bwd(
+        _p(logits), logits_type, T, E, ldl, topk, int(renorm), _p(expert_ids), _p(weights), _p(dweights), _p(counts),
+        balance_coef, _p(dloss), _p(dlogits), ldd, _stream(stream)))
+
+
+def bsq_moe_combine(y, R, H, ldy, rows, weights, T, topk, out, ldo, stream=None):
+    return _check("bsq_moe_combine", lib().bsq_moe_combine(_p(y), R, H, ldy, _p(rows), _p(weights), T, topk, _p(out),
+                                                           ldo, _stream(stream)))
+
+
+def bsq_moe_combine_bwd(dout, ldo, y, ldy, y_codes, y_sf, R, H, rows, weights, T, topk, dy, lddy, dweights,
+                        stream=None):
+    return _check("bsq_moe_combine_bwd", lib().bsq_moe_combine_bwd(
+        _p(dout), ldo, _p(y), ldy, _p(y_codes), _p(y_sf), R, H, _p(rows), _p(weights), T, topk, _p(dy), lddy,
+        _p(dweights), _stream(stream)))
+
+
+def bsq_swiglu_ckpt(u, M, F, ldu, n_rows, h, ldh, codes, sf, amax, stream=None):
+    return _check("bsq_swiglu_ckpt", lib().bsq_swiglu_ckpt(_p(u), M, F, ldu, _p(n_rows), _p(h), ldh, _p(codes),
+                                                           _p(sf), _p(amax), _stream(stream)))
+
+
+def bsq_swiglu_ckpt_bwd(dh, lddh, codes, sf, M, F, n_rows, du, lddu, h, ldh, stream=None):
+    return _check("bsq_swiglu_ckpt_bwd", lib().bsq_swiglu_ckpt_bwd(
+        _p(dh), lddh, _p(codes), _p(sf), M, F, _p(n_rows), _p(du), lddu, _p(h), ldh, _stream(stream)))

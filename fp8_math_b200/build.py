@@ -23,9 +23,10 @@ COMMON = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcom
 SOURCES = {
     "quant.cu": ["--fmad=false"],
     "gemm.cu": [],
+    "moe.cu": [],
     "api.cu": [],
 }
-HEADERS = ["common.cuh", "devcache.h", "nvfp4.cuh", "quant.cuh", "gemm.cuh", "sm100.cuh"]
+HEADERS = ["common.cuh", "devcache.h", "nvfp4.cuh", "quant.cuh", "gemm.cuh", "moe.cuh", "sm100.cuh"]
 
 
 def _mtime(p):

@@ -8,6 +8,7 @@
 
 #include "common.cuh"
 #include "gemm.cuh"
+#include "moe.cuh"
 #include "quant.cuh"
 
 namespace {
@@ -560,6 +561,145 @@ int bsq_grouped_gemm_nvfp4_out(int fmt, int G, const int32_t *row_off, const int
     g.q_codes = out_codes; g.q_sf = out_sf; g.q_sg = out_gs;
     g.q_amax = reinterpret_cast<unsigned int *>(out_amax); g.q_fos = four_over_six != 0;
     return bsq::launch_gemm(g, s);
+}
+
+// ------------------------------------------------------------ mixture-of-experts training step
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// T tokens, E experts, k slots: BSQ_OK, or why the router's kernels do not take them.
+static int route_sizes(int64_t T, int64_t E, int topk) {
+    if (T < 0 || E < 1 || topk < 1 || topk > E) return BSQ_ERR_INVALID;
+    // row numbers, and scale-factor rows padded to 128 per expert, are int32
+    if (E > bsq::kRouteMaxExperts || topk > bsq::kRouteMaxTopk || T >= (int64_t(1) << 31) ||
+        T * topk + 128 * E >= (int64_t(1) << 31))
+        return BSQ_ERR_UNSUPPORTED;
+    return BSQ_OK;
+}
+
+size_t bsq_moe_route_workspace(int64_t T, int64_t E) {
+    if (route_sizes(T, E, 1) != BSQ_OK) return 0;
+    return (size_t)bsq::route_workspace(T, E).bytes;
+}
+
+int bsq_moe_route(const void *logits, int logits_type, int64_t T, int64_t E, int64_t ldl, const uint8_t *token_mask,
+                  int topk, int renorm, int32_t *ids, float *weights, int32_t *rows, int32_t *row_index,
+                  int32_t *row_off, int32_t *sf_row_off, int32_t *counts, float *prob_sums, float balance_coef,
+                  float *loss, void *workspace, size_t workspace_bytes, void *stream) {
+    if ((logits_type != BSQ_OUT_F32 && logits_type != BSQ_OUT_BF16) || !row_off || !sf_row_off || !counts ||
+        !workspace || ldl < E)
+        return BSQ_ERR_INVALID;
+    if (int st = route_sizes(T, E, topk)) return st;
+    if (T > 0 && (!logits || !ids || !weights || !rows || !row_index)) return BSQ_ERR_INVALID;
+    if (workspace_bytes < bsq_moe_route_workspace(T, E)) return BSQ_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(logits) & (logits_type == BSQ_OUT_F32 ? 3u : 1u)) || !aligned4(ids) ||
+        !aligned4(weights) || !aligned4(rows) || !aligned4(row_index) || !aligned4(row_off) || !aligned4(sf_row_off) ||
+        !aligned4(counts) || !aligned4(prob_sums) || !aligned4(loss) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return BSQ_ERR_ALIGN;
+    DeviceState *d;
+    if (int st = device_state(&d)) return st;
+    bsq::RouteArgs a{};
+    a.logits = logits; a.bf16 = logits_type == BSQ_OUT_BF16; a.T = T; a.E = E; a.ldl = ldl; a.mask = token_mask;
+    a.topk = topk; a.renorm = renorm != 0; a.ids = ids; a.weights = weights; a.rows = rows; a.row_index = row_index;
+    a.row_off = row_off; a.sf_row_off = sf_row_off; a.counts = counts; a.prob_sums = prob_sums;
+    a.coef = balance_coef; a.loss = loss; a.ws = static_cast<uint8_t *>(workspace);
+    return bsq::launch_moe_route(a, d->num_sms, static_cast<cudaStream_t>(stream)) ? BSQ_ERR_CUDA : BSQ_OK;
+}
+
+int bsq_moe_route_bwd(const void *logits, int logits_type, int64_t T, int64_t E, int64_t ldl, int topk, int renorm,
+                      const int32_t *ids, const float *weights, const float *dweights, const int32_t *counts,
+                      float balance_coef, const float *dloss, void *dlogits, int64_t ldd, void *stream) {
+    if ((logits_type != BSQ_OUT_F32 && logits_type != BSQ_OUT_BF16) || ldl < E || ldd < E ||
+        (dloss && !counts))
+        return BSQ_ERR_INVALID;
+    if (int st = route_sizes(T, E, topk)) return st;
+    if (T > 0 && (!logits || !ids || !weights || !dlogits)) return BSQ_ERR_INVALID;
+    const uintptr_t low = logits_type == BSQ_OUT_F32 ? 3u : 1u;
+    if ((reinterpret_cast<uintptr_t>(logits) & low) || (reinterpret_cast<uintptr_t>(dlogits) & low) ||
+        !aligned4(ids) || !aligned4(weights) || !aligned4(dweights) || !aligned4(counts) || !aligned4(dloss))
+        return BSQ_ERR_ALIGN;
+    DeviceState *d;
+    if (int st = device_state(&d)) return st;
+    if (T == 0) return BSQ_OK;
+    bsq::RouteBwdArgs a{};
+    a.logits = logits; a.bf16 = logits_type == BSQ_OUT_BF16; a.T = T; a.E = E; a.ldl = ldl; a.topk = topk;
+    a.renorm = renorm != 0; a.ids = ids; a.weights = weights; a.dweights = dweights; a.counts = counts;
+    a.coef = balance_coef; a.dloss = dloss; a.dlogits = dlogits; a.ldd = ldd;
+    return bsq::launch_moe_route_bwd(a, d->num_sms, static_cast<cudaStream_t>(stream)) ? BSQ_ERR_CUDA : BSQ_OK;
+}
+
+int bsq_moe_combine(const void *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
+                    int64_t T, int topk, void *out, int64_t ldo, void *stream) {
+    if (R < 0 || H < 0 || H % 8 || ldy < H || ldo < H || T < 0 || topk < 1) return BSQ_ERR_INVALID;
+    if (topk > bsq::kRouteMaxTopk || T >= (int64_t(1) << 31) || H > (int64_t(1) << 25)) return BSQ_ERR_UNSUPPORTED;
+    if (T > 0 && H > 0 && (!rows || !out || (R > 0 && !y))) return BSQ_ERR_INVALID;
+    if (!aligned16(y) || !aligned16(out) || ldy % 8 || ldo % 8 || !aligned4(rows) || !aligned4(weights))
+        return BSQ_ERR_ALIGN;
+    DeviceState *d;
+    if (int st = device_state(&d)) return st;
+    if (T == 0 || H == 0) return BSQ_OK;
+    return bsq::launch_moe_combine(static_cast<const uint16_t *>(y), R, H, ldy, rows, weights, T, topk,
+                                   static_cast<uint16_t *>(out), ldo, d->num_sms, static_cast<cudaStream_t>(stream))
+               ? BSQ_ERR_CUDA
+               : BSQ_OK;
+}
+
+int bsq_moe_combine_bwd(const void *dout, int64_t ldo, const void *y, int64_t ldy, const uint8_t *y_codes,
+                        const uint8_t *y_sf, int64_t R, int64_t H, const int32_t *rows, const float *weights,
+                        int64_t T, int topk, void *dy, int64_t lddy, float *dweights, void *stream) {
+    if (R < 0 || H < 0 || H % 8 || ldo < H || lddy < H || T < 0 || topk < 1) return BSQ_ERR_INVALID;
+    if (y && (y_codes || y_sf)) return BSQ_ERR_INVALID;       // one form of y, not both
+    if (!y && (!y_codes != !y_sf)) return BSQ_ERR_INVALID;    // codes and scales come together
+    if (y ? ldy < H : H % 32 != 0) return BSQ_ERR_INVALID;
+    if (topk > bsq::kRouteMaxTopk || T >= (int64_t(1) << 31) || H > (int64_t(1) << 25)) return BSQ_ERR_UNSUPPORTED;
+    if (T > 0 && (!rows || !weights || !dweights)) return BSQ_ERR_INVALID;
+    if (T > 0 && H > 0 && (!dout || (R > 0 && (!dy || (!y && !y_codes))))) return BSQ_ERR_INVALID;
+    if (!aligned16(dout) || !aligned16(y) || !aligned16(y_codes) || !aligned16(y_sf) || !aligned16(dy) || ldo % 8 ||
+        (y && ldy % 8) || lddy % 8 || !aligned4(rows) || !aligned4(weights) || !aligned4(dweights))
+        return BSQ_ERR_ALIGN;
+    DeviceState *d;
+    if (int st = device_state(&d)) return st;
+    if (T == 0) return BSQ_OK;
+    return bsq::launch_moe_combine_bwd(static_cast<const uint16_t *>(dout), ldo, static_cast<const uint16_t *>(y), ldy,
+                                       y_codes, y_sf, R, H, rows, weights, T, topk, static_cast<uint16_t *>(dy), lddy,
+                                       dweights, d->num_sms, static_cast<cudaStream_t>(stream))
+               ? BSQ_ERR_CUDA
+               : BSQ_OK;
+}
+
+int bsq_swiglu_ckpt(const void *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, void *h, int64_t ldh,
+                    uint8_t *codes, uint8_t *sf, float *amax, void *stream) {
+    if (M < 0 || F < 0 || F % 32 || ldu < 2 * F || ldh < F) return BSQ_ERR_INVALID;
+    if (M > 0 && F > 0 && (!u || !h || !codes || !sf)) return BSQ_ERR_INVALID;
+    if (!aligned16(u) || !aligned16(h) || !aligned16(codes) || !aligned16(sf) || ldu % 8 || ldh % 8 ||
+        !aligned4(n_rows) || !aligned4(amax))
+        return BSQ_ERR_ALIGN;
+    DeviceState *d;
+    if (int st = device_state(&d)) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (amax && cudaMemsetAsync(amax, 0, sizeof(float), s) != cudaSuccess) return BSQ_ERR_CUDA;
+    if (M == 0 || F == 0) return BSQ_OK;
+    return bsq::launch_swiglu_ckpt(static_cast<const uint16_t *>(u), M, F, ldu, n_rows, static_cast<uint16_t *>(h),
+                                   ldh, codes, sf, reinterpret_cast<unsigned int *>(amax), d->num_sms, s)
+               ? BSQ_ERR_CUDA
+               : BSQ_OK;
+}
+
+int bsq_swiglu_ckpt_bwd(const void *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M, int64_t F,
+                        const int32_t *n_rows, void *du, int64_t lddu, void *h, int64_t ldh, void *stream) {
+    if (M < 0 || F < 0 || F % 32 || lddh < F || lddu < 2 * F || (h && ldh < F)) return BSQ_ERR_INVALID;
+    if (M > 0 && F > 0 && (!dh || !codes || !sf || !du)) return BSQ_ERR_INVALID;
+    if (!aligned16(dh) || !aligned16(codes) || !aligned16(sf) || !aligned16(du) || !aligned16(h) || lddh % 8 ||
+        lddu % 8 || (h && ldh % 8) || !aligned4(n_rows))
+        return BSQ_ERR_ALIGN;
+    DeviceState *d;
+    if (int st = device_state(&d)) return st;
+    if (M == 0 || F == 0) return BSQ_OK;
+    return bsq::launch_swiglu_ckpt_bwd(static_cast<const uint16_t *>(dh), lddh, codes, sf, M, F, n_rows,
+                                       static_cast<uint16_t *>(du), lddu, static_cast<uint16_t *>(h), ldh, d->num_sms,
+                                       static_cast<cudaStream_t>(stream))
+               ? BSQ_ERR_CUDA
+               : BSQ_OK;
 }
 
 int bsq_check(void *stream) {

@@ -1,0 +1,705 @@
+// moe.cu -- kernels of a mixture-of-experts layer's training step that stand
+// between the quantizers and the grouped GEMM: the router (top-k, weights,
+// counts, row order, balance loss) and its gradient, the combine of expert
+// rows in bf16 and its gradients, the gated SiLU whose input is kept in MXFP8
+// for the backward pass.  All sums are in fp32 and in a fixed order, so a call
+// gives the same bits every time.
+#include <algorithm>
+
+#include "common.cuh"
+#include "moe.cuh"
+
+namespace bsq {
+
+namespace {
+
+constexpr unsigned kFull = 0xFFFFFFFFu;
+constexpr int kChunk = 64;  // tokens of one router CTA: their choice of an expert is one 64-bit mask
+
+BSQ_DEV float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+BSQ_DEV float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+BSQ_DEV uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&b);
+}
+BSQ_DEV float load_logit(const float *p) { return __ldg(p); }
+BSQ_DEV float load_logit(const uint16_t *p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
+BSQ_DEV void store_logit(float *p, float v) { *p = v; }
+BSQ_DEV void store_logit(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
+
+// Unsigned keys in the order of the floats (-0 taken as +0, so that equal
+// logits have equal keys).  Key 0 marks an expert that has been taken.
+BSQ_DEV uint32_t order_key(float z) {
+    const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+BSQ_DEV float key_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+
+// ------------------------------------------------------------------ router
+// Pass 1.  A CTA takes kChunk consecutive tokens, a warp one token at a time;
+// lane l holds the logits of experts l, l + 32, ...  k rounds of "largest
+// key, then lowest expert that has it" (two warp reductions) give the top-k
+// by (-logit, expert).  A slot whose best logit is -inf stays empty.  The
+// softmax sum runs over the same registers.  The chosen experts go into one
+// 64-bit mask of tokens per expert, whose population count is the chunk's
+// count and whose bits below a token are that token's rank in the chunk:
+// the order "by expert, then token" needs no sort.  Row E of the counts is
+// the number of tokens with at least one expert.
+template <typename In, int EPL>
+__global__ void __launch_bounds__(256) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
+                                                         const uint8_t *__restrict__ mask, int k, int renorm,
+                                                         int want_p, int32_t *__restrict__ ids,
+                                                         float *__restrict__ weights, int32_t *__restrict__ rows,
+                                                         int64_t nchunk, uint32_t *__restrict__ hist,
+                                                         float *__restrict__ psum) {
+    extern __shared__ unsigned long long smem[];
+    unsigned int *words = reinterpret_cast<unsigned int *>(smem);               // [(E + 1) * 2]
+    uint16_t *sel = reinterpret_cast<uint16_t *>(words + 2 * (E + 1));          // [kChunk][k]
+    float *red = reinterpret_cast<float *>(sel + kChunk * k);                   // [8][E] when want_p
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < 2 * (E + 1); i += 256) words[i] = 0;
+    __syncthreads();
+    const int64_t t0 = (int64_t)blockIdx.x * kChunk;
+    float acc[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; i++) acc[i] = 0.0f;
+    for (int tl = warp; tl < kChunk; tl += 8) {
+        const int64_t t = t0 + tl;
+        if (t >= T) break;
+        const bool live = !mask || __ldg(mask + t) != 0;
+        uint32_t key[EPL];
+        float z[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            const int e = i * 32 + lane;
+            const bool in = live && e < E;
+            z[i] = in ? load_logit(logits + t * ldl + e) : -INFINITY;
+            key[i] = in ? order_key(z[i]) : 0u;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) top = fmaxf(top, z[i]);
+        top = warp_max(top);
+        float sum_all = 0.0f;
+        if (want_p || !renorm) {
+            const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                z[i] = expf(z[i] - base);
+                sum_all += z[i];
+            }
+            sum_all = warp_sum(sum_all);
+            const float inv = sum_all > 0.0f ? 1.0f / sum_all : 0.0f;
+            if (want_p)
+#pragma unroll
+                for (int i = 0; i < EPL; i++) acc[i] += z[i] * inv;
+        }
+        uint32_t my_key = 0;
+        int my_e = -1;
+        for (int j = 0; j < k; j++) {
+            uint32_t best = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) best = max(best, key[i]);
+            best = __reduce_max_sync(kFull, best);
+            if (best <= kKeyNegInf) break;
+            unsigned int e = 0xFFFFu;
+#pragma unroll
+            for (int i = EPL - 1; i >= 0; i--)
+                if (key[i] == best) e = i * 32 + lane;
+            e = __reduce_min_sync(kFull, e);
+#pragma unroll
+            for (int i = 0; i < EPL; i++)
+                if (i * 32 + lane == (int)e) key[i] = 0;
+            if (lane == j) {
+                my_key = best;
+                my_e = (int)e;
+            }
+        }
+        float x = my_e >= 0 ? expf(key_value(my_key) - top) : 0.0f;
+        const float sum = renorm ? warp_sum(x) : sum_all;
+        if (lane < k) {
+            ids[t * k + lane] = my_e;
+            weights[t * k + lane] = my_e >= 0 ? x / sum : 0.0f;
+            sel[tl * k + lane] = (uint16_t)my_e;
+            if (my_e >= 0) atomicOr(&words[2 * my_e + (tl >> 5)], 1u << (tl & 31));
+            if (lane == 0 && my_e >= 0) atomicOr(&words[2 * E + (tl >> 5)], 1u << (tl & 31));
+        }
+    }
+    if (want_p) {
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (i * 32 + lane < E) red[warp * E + i * 32 + lane] = acc[i];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < kChunk * k; i += 256) {
+        const int tl = i / k;
+        if (t0 + tl >= T) break;
+        const int e = (int16_t)sel[i];
+        int rank = -1;
+        if (e >= 0) {
+            const unsigned long long below = smem[e] & ((1ull << tl) - 1ull);
+            rank = __popcll(below);
+        }
+        rows[t0 * k + i] = rank;
+    }
+    for (int e = threadIdx.x; e <= E; e += 256) {
+        const unsigned long long m = smem[e];
+        // count in the low byte, the chunk's first token of the expert above it
+        hist[(int64_t)e * nchunk + blockIdx.x] = (uint32_t)__popcll(m) | (m ? (uint32_t)(__ffsll(m) - 1) << 8 : 0u);
+        if (want_p && e < E) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 8; w++) v += red[w * E + e];
+            psum[(int64_t)e * nchunk + blockIdx.x] = v;
+        }
+    }
+}
+
+// Pass 2.  One CTA per expert (and one for the token count): its counts per
+// chunk become exclusive prefixes in place, their total goes to counts[e];
+// the first token that chose e, and the sum of its probabilities, go along.
+__global__ void __launch_bounds__(256) route_scan_kernel(uint32_t *__restrict__ hist, const float *__restrict__ psum,
+                                                         int64_t nchunk, int E, int32_t *__restrict__ counts,
+                                                         int32_t *__restrict__ first, float *__restrict__ psum_total) {
+    grid_dependency_wait();
+    __shared__ int wsum[8];
+    __shared__ float fsum[8];
+    __shared__ int sfirst;
+    const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t *h = hist + (int64_t)e * nchunk;
+    if (threadIdx.x == 0) sfirst = 0x7FFFFFFF;
+    __syncthreads();
+    int carry = 0;
+    float p = 0.0f;
+    for (int64_t c0 = 0; c0 < nchunk; c0 += 256) {
+        const int64_t c = c0 + threadIdx.x;
+        const uint32_t v = c < nchunk ? h[c] : 0u;
+        const int n = (int)(v & 0xFFu);
+        if (n) atomicMin(&sfirst, (int)(c * kChunk) + (int)(v >> 8));
+        if (psum && e < E && c < nchunk) p += psum[(int64_t)e * nchunk + c];
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) wsum[warp] = s;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < 8; w++) {
+            if (w < warp) before += wsum[w];
+            all += wsum[w];
+        }
+        if (c < nchunk) h[c] = (uint32_t)(carry + before + s - n);
+        carry += all;
+        __syncthreads();
+    }
+    p = warp_sum(p);
+    if (lane == 0) fsum[warp] = p;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        counts[e] = carry;
+        if (e < E) {
+            first[e] = sfirst;
+            if (psum) {
+                float v = 0.0f;
+                for (int w = 0; w < 8; w++) v += fsum[w];
+                psum_total[e] = v;
+            }
+        }
+    }
+}
+
+// Exclusive scan over e < E of counts[e] (PAD128: each rounded up to 128)
+// into off[0..E], by one CTA of 256 threads holding four experts each.
+template <bool PAD128>
+BSQ_DEV void scan_counts(const int32_t *counts, int E, int32_t *off, int *wsum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int n[4], s = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int e = threadIdx.x * 4 + i;
+        n[i] = e < E ? counts[e] : 0;
+        if (PAD128) n[i] = (n[i] + 127) & ~127;
+        s += n[i];
+    }
+    int inc = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int at = inc - s;
+    for (int w = 0; w < warp; w++) at += wsum[w];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int e = threadIdx.x * 4 + i;
+        if (e <= E) off[e] = at;
+        at += n[i];
+    }
+    if (E == 1024 && threadIdx.x == 255) off[E] = at;
+    __syncthreads();
+}
+
+// Pass 3.  Row of a slot = its expert's offset + the chunk's prefix + the
+// rank inside the chunk; the rows past the last routed one repeat the first
+// row's token.  CTA 0 also writes the offsets and the loss.
+__global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ rows,
+                                                          int64_t T, int k, int E, int64_t nchunk,
+                                                          const uint32_t *__restrict__ hist,
+                                                          const int32_t *__restrict__ counts,
+                                                          const int32_t *__restrict__ first,
+                                                          const float *__restrict__ psum_total, float coef,
+                                                          int32_t *__restrict__ row_index,
+                                                          int32_t *__restrict__ row_off,
+                                                          int32_t *__restrict__ sf_row_off,
+                                                          float *__restrict__ prob_sums, float *__restrict__ loss) {
+    grid_dependency_wait();
+    __shared__ int32_t off[kRouteMaxExperts + 1];
+    __shared__ int wsum[8];
+    __shared__ int first_token;
+    if (threadIdx.x == 0) first_token = 0;
+    scan_counts<false>(counts, E, off, wsum);
+    for (int e = threadIdx.x; e < E; e += 256)
+        if (off[e] == 0 && off[e + 1] > 0) first_token = first[e];  // one expert only
+    __syncthreads();
+    const int64_t n = T * k, total = off[E];
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int e = ids[i];
+        const int64_t t = i / k;
+        if (e >= 0) {
+            const int row = off[e] + (int)hist[(int64_t)e * nchunk + t / kChunk] + rows[i];
+            rows[i] = row;
+            row_index[row] = (int32_t)t;
+        }
+        if (i >= total) row_index[i] = first_token;
+    }
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e <= E; e += 256) row_off[e] = off[e];
+        float part = 0.0f;
+        if (psum_total)
+            for (int e = threadIdx.x; e < E; e += 256) {
+                const float p = psum_total[e];
+                if (prob_sums) prob_sums[e] = p;
+                part += (float)counts[e] * p;
+            }
+        __syncthreads();
+        if (loss) {
+            __shared__ float fsum[8];
+            part = warp_sum(part);
+            if ((threadIdx.x & 31) == 0) fsum[threadIdx.x >> 5] = part;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float v = 0.0f;
+                for (int w = 0; w < 8; w++) v += fsum[w];
+                const float tokens = (float)counts[E];
+                // E / (k n^2) * sum c_e sum_t p_te, by two divisions: n^2 may pass 2^24
+                *loss = counts[E] > 0 ? coef * (float)E * (v / tokens) / ((float)k * tokens) : 0.0f;
+            }
+        }
+        scan_counts<true>(counts, E, off, wsum);
+        for (int e = threadIdx.x; e <= E; e += 256) sf_row_off[e] = off[e];
+    }
+}
+
+// ------------------------------------------------------------------ router, backward
+// One warp per token.  With q the weights' distribution (the softmax over all
+// experts, or over the chosen ones) and a_e = dL/dweight of expert e (zero
+// where it was not chosen): dz_e = q_e (a_e - sum q a).  The balance loss adds
+// the softmax's gradient of sum_e b_e p_e with b_e = dloss coef E c_e / (k n^2).
+template <typename In, int EPL>
+__global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
+                                                        int k, int renorm, const int32_t *__restrict__ ids,
+                                                        const float *__restrict__ weights,
+                                                        const float *__restrict__ dweights,
+                                                        const int32_t *__restrict__ counts, float coef,
+                                                        const float *__restrict__ dloss, In *__restrict__ dlogits,
+                                                        int64_t ldd) {
+    const int lane = threadIdx.x & 31;
+    float bscale = 0.0f;
+    if (dloss) {
+        const int n = __ldg(counts + E);
+        bscale = n > 0 ? __ldg(dloss) * coef * (float)E / (float)n / ((float)k * (float)n) : 0.0f;
+    }
+    const bool need_p = !renorm || dloss;
+    const int64_t stride = (int64_t)gridDim.x * 8;
+    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += stride) {
+        int e_j = -1;
+        float w_j = 0.0f, a_j = 0.0f;
+        if (lane < k) {
+            e_j = __ldg(ids + t * k + lane);
+            if ((unsigned)e_j >= (unsigned)E) e_j = -1;
+            if (e_j >= 0) {
+                w_j = __ldg(weights + t * k + lane);
+                a_j = dweights ? __ldg(dweights + t * k + lane) : 0.0f;
+            }
+        }
+        const bool live = __any_sync(kFull, e_j >= 0);
+        const float dot = warp_sum(w_j * a_j);  // sum over chosen of q a: both kinds of q have q_ej = w_j
+        float d[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; i++) d[i] = 0.0f;
+        if (live && need_p) {
+            float p[EPL], top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                const int e = i * 32 + lane;
+                p[i] = e < E ? load_logit(logits + t * ldl + e) : -INFINITY;
+                top = fmaxf(top, p[i]);
+            }
+            top = warp_max(top);
+            float s = 0.0f, pb = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                p[i] = expf(p[i] - top);
+                s += p[i];
+            }
+            const float inv = 1.0f / warp_sum(s);
+            float b[EPL];
+#pragma unroll
+            for (int i = 0; i < EPL; i++) {
+                const int e = i * 32 + lane;
+                p[i] *= inv;
+                b[i] = dloss && e < E ? bscale * (float)__ldg(counts + e) : 0.0f;
+                pb += p[i] * b[i];
+            }
+            pb = warp_sum(pb);
+            const float sub = pb + (renorm ? 0.0f : dot);
+#pragma unroll
+            for (int i = 0; i < EPL; i++) d[i] = p[i] * (b[i] - sub);
+        }
+        // the chosen experts' own term: w_j (a_j - dot), or w_j a_j where dot went over all experts
+        const float own = renorm ? w_j * (a_j - dot) : w_j * a_j;
+        for (int j = 0; j < k; j++) {
+            const int e = __shfl_sync(kFull, e_j, j);
+            const float v = __shfl_sync(kFull, own, j);
+#pragma unroll
+            for (int i = 0; i < EPL; i++)
+                if (i * 32 + lane == e) d[i] += v;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; i++)
+            if (i * 32 + lane < E) store_logit(dlogits + t * ldd + i * 32 + lane, d[i]);
+    }
+}
+
+// ------------------------------------------------------------------ combine
+// out[t] = sum_j w_tj y[rows_tj]: a CTA of 128 threads takes 1024 columns of
+// one token, each thread eight of them over all k rows.
+__global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict__ y, int64_t R, int64_t H, int64_t ldy,
+                                                      const int32_t *__restrict__ rows,
+                                                      const float *__restrict__ weights, int k,
+                                                      uint16_t *__restrict__ out, int64_t ldo) {
+    const int64_t t = blockIdx.x;
+    const int64_t c = ((int64_t)blockIdx.y * 128 + threadIdx.x) * 8;
+    if (c >= H) return;
+    float acc[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) acc[i] = 0.0f;
+    for (int j = 0; j < k; j++) {
+        const int64_t r = __ldg(rows + t * k + j);
+        if (r < 0 || r >= R) continue;
+        const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
+        float v[8];
+        load8_bf16(y + r * ldy + c, v);
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc[i] += w * v[i];
+    }
+    *reinterpret_cast<uint4 *>(out + t * ldo + c) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
+                                                               pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
+}
+
+// Eight values of an MXFP8 row: codes times 2^(scale code - 127).
+BSQ_DEV void load8_mx(const uint8_t *codes, const uint8_t *sf, int64_t r, int64_t c, int64_t K, float v[8]) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(codes + r * K + c));
+    const float scale = exp2i((int)__ldg(sf + sf_offset(r, c >> 5, K >> 5)) - 127);
+    e4m3x2_to_f32(q.x & 0xFFFFu, v[0], v[1]);
+    e4m3x2_to_f32(q.x >> 16, v[2], v[3]);
+    e4m3x2_to_f32(q.y & 0xFFFFu, v[4], v[5]);
+    e4m3x2_to_f32(q.y >> 16, v[6], v[7]);
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] *= scale;
+}
+
+// dy[rows_tj] = w_tj dout_t and dw_tj = <dout_t, y[rows_tj]>: one CTA per
+// token, row by row; the dot product is summed per warp, then over the warps.
+template <bool MX>
+__global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__restrict__ dout, int64_t ldo,
+                                                          const uint16_t *__restrict__ y, int64_t ldy,
+                                                          const uint8_t *__restrict__ codes,
+                                                          const uint8_t *__restrict__ sf, int64_t R, int64_t H,
+                                                          const int32_t *__restrict__ rows,
+                                                          const float *__restrict__ weights, int k,
+                                                          uint16_t *__restrict__ dy, int64_t lddy,
+                                                          float *__restrict__ dweights) {
+    __shared__ float part[kRouteMaxTopk][8];
+    const int64_t t = blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int j = 0; j < k; j++) {
+        const int64_t r = __ldg(rows + t * k + j);
+        float dot = 0.0f;
+        if (r >= 0 && r < R) {
+            const float w = __ldg(weights + t * k + j);
+            for (int64_t c = threadIdx.x * 8; c < H; c += 256 * 8) {
+                float d[8], v[8];
+                load8_bf16(dout + t * ldo + c, d);
+                if (MX) load8_mx(codes, sf, r, c, H, v);
+                else load8_bf16(y + r * ldy + c, v);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    dot += d[i] * v[i];
+                    d[i] *= w;
+                }
+                *reinterpret_cast<uint4 *>(dy + r * lddy + c) = make_uint4(
+                    pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+            }
+        }
+        dot = warp_sum(dot);
+        if (lane == 0) part[j][warp] = dot;
+    }
+    __syncthreads();
+    if (threadIdx.x < k) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; w++) s += part[threadIdx.x][w];
+        dweights[t * k + threadIdx.x] = s;
+    }
+}
+
+// ------------------------------------------------------------------ gated SiLU with an MXFP8 checkpoint
+// sigmoid(g) and its complement's product form: e = exp(-|g|) never overflows.
+BSQ_DEV float sigmoid(float g) {
+    const float e = expf(-fabsf(g));
+    const float r = 1.0f / (1.0f + e);
+    return g >= 0.0f ? r : e * r;
+}
+
+// Row-wise MXFP8 of eight values, four lanes per block of 32 (the bytes of
+// bsq_quant_mxfp8 with nearest rounding): returns the codes, *scale_code the
+// block's E8M0 code.
+BSQ_DEV uint2 mx_encode_quad(const float v[8], uint32_t *scale_code) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[i]));
+    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+    if (m == 0.0f) {
+        *scale_code = 0;
+        return make_uint2(0u, 0u);  // an all-zero block has +0 codes
+    }
+    const int E = max(floor_log2(m) - 8, -127);
+    *scale_code = (uint32_t)(E + 127);
+    const float inv = exp2i(-E);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) s[i] = fminf(fmaxf(v[i] * inv, -448.0f), 448.0f);
+    return make_uint2(cvt_e4m3x2(s[0], s[1]) | (cvt_e4m3x2(s[2], s[3]) << 16),
+                      cvt_e4m3x2(s[4], s[5]) | (cvt_e4m3x2(s[6], s[7]) << 16));
+}
+
+__global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F,
+                                                          int64_t ldu, const int32_t *__restrict__ n_rows,
+                                                          uint16_t *__restrict__ h, int64_t ldh,
+                                                          uint8_t *__restrict__ codes, uint8_t *__restrict__ sf,
+                                                          unsigned int *__restrict__ amax) {
+    __shared__ float part[8];
+    const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
+    const int64_t per = F / 8, n = rows * per;
+    float top = 0.0f;
+    // n is a multiple of 4: the four lanes of a block leave the loop together; the shuffles want whole warps
+    const int64_t round = (n + 31) / 32 * 32;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < round; i += (int64_t)gridDim.x * 256) {
+        const bool in = i < n;
+        const int64_t r = in ? i / per : 0, c = in ? (i - r * per) * 8 : 0;
+        float g[8], v[8];
+        load8_bf16(u + r * ldu + c, g);
+        load8_bf16(u + r * ldu + F + c, v);
+        uint32_t sg, sv;
+        const uint2 cg = mx_encode_quad(g, &sg), cv = mx_encode_quad(v, &sv);
+        if (!in) continue;
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const float a = g[2 * q] * sigmoid(g[2 * q]) * v[2 * q];
+            const float b = g[2 * q + 1] * sigmoid(g[2 * q + 1]) * v[2 * q + 1];
+            o[q] = pack_bf16(a, b);
+            top = fmaxf(top, fmaxf(fabsf(bf16_lo(o[q])), fabsf(bf16_hi(o[q]))));
+        }
+        *reinterpret_cast<uint4 *>(h + r * ldh + c) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint2 *>(codes + r * 2 * F + c) = cg;
+        *reinterpret_cast<uint2 *>(codes + r * 2 * F + F + c) = cv;
+        if ((threadIdx.x & 3) == 0) {
+            sf[sf_offset(r, c >> 5, F >> 4)] = (uint8_t)sg;
+            sf[sf_offset(r, (F + c) >> 5, F >> 4)] = (uint8_t)sv;
+        }
+    }
+    if (amax) {
+        top = warp_max(top);
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 8; w++) top = fmaxf(top, part[w]);
+            atomicMax(amax, __float_as_uint(top));  // non-negative floats order as their bits
+        }
+    }
+}
+
+// From the checkpoint's g and u: du = dh g s, dg = dh u s (1 + g (1 - s)),
+// and, when h is wanted, h = g s u again.
+__global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__restrict__ dh, int64_t lddh,
+                                                              const uint8_t *__restrict__ codes,
+                                                              const uint8_t *__restrict__ sf, int64_t M, int64_t F,
+                                                              const int32_t *__restrict__ n_rows,
+                                                              uint16_t *__restrict__ du, int64_t lddu,
+                                                              uint16_t *__restrict__ h, int64_t ldh) {
+    const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
+    const int64_t per = F / 8, n = rows * per;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per, c = (i - r * per) * 8;
+        float d[8], g[8], v[8], x[8], y[8], w[8];
+        load8_bf16(dh + r * lddh + c, d);
+        load8_mx(codes, sf, r, c, 2 * F, g);
+        load8_mx(codes, sf, r, F + c, 2 * F, v);
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            const float s = sigmoid(g[q]), gs = g[q] * s;
+            x[q] = d[q] * v[q] * s * (1.0f + g[q] * (1.0f - s));
+            y[q] = d[q] * gs;
+            w[q] = gs * v[q];
+        }
+        *reinterpret_cast<uint4 *>(du + r * lddu + c) =
+            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        *reinterpret_cast<uint4 *>(du + r * lddu + F + c) =
+            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        if (h)
+            *reinterpret_cast<uint4 *>(h + r * ldh + c) =
+                make_uint4(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7]));
+    }
+}
+
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+int launched() { return cudaGetLastError() == cudaSuccess ? 0 : 1; }
+
+template <typename In>
+int route_topk(const RouteArgs &a, const RouteWorkspace &w, int want_p, cudaStream_t s) {
+    const int E = (int)a.E, k = a.topk;
+    // at most 45064 bytes (1024 experts, 32 slots): within the default limit
+    const size_t smem = 8 * (size_t)(E + 1) + 2 * kChunk * (size_t)k + (want_p ? 32 * (size_t)E : 0);
+    auto run = [&](auto kern) {
+        kern<<<(unsigned)w.nchunk, 256, smem, s>>>(
+            static_cast<const In *>(a.logits), a.T, E, a.ldl, a.mask, k, a.renorm, want_p, a.ids, a.weights, a.rows,
+            w.nchunk, reinterpret_cast<uint32_t *>(a.ws + w.hist), reinterpret_cast<float *>(a.ws + w.psum));
+        return launched();
+    };
+    if (E <= 32) return run(route_topk_kernel<In, 1>);
+    if (E <= 64) return run(route_topk_kernel<In, 2>);
+    if (E <= 128) return run(route_topk_kernel<In, 4>);
+    if (E <= 256) return run(route_topk_kernel<In, 8>);
+    if (E <= 512) return run(route_topk_kernel<In, 16>);
+    return run(route_topk_kernel<In, 32>);
+}
+
+template <typename In>
+int route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
+    const unsigned grid = (unsigned)std::min<int64_t>((a.T + 7) / 8, (int64_t)num_sms * 16);
+    auto run = [&](auto kern) {
+        kern<<<grid, 256, 0, s>>>(static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, a.topk, a.renorm, a.ids,
+                                  a.weights, a.dweights, a.counts, a.coef, a.dloss, static_cast<In *>(a.dlogits),
+                                  a.ldd);
+        return launched();
+    };
+    if (a.E <= 32) return run(route_bwd_kernel<In, 1>);
+    if (a.E <= 64) return run(route_bwd_kernel<In, 2>);
+    if (a.E <= 128) return run(route_bwd_kernel<In, 4>);
+    if (a.E <= 256) return run(route_bwd_kernel<In, 8>);
+    if (a.E <= 512) return run(route_bwd_kernel<In, 16>);
+    return run(route_bwd_kernel<In, 32>);
+}
+
+}  // namespace
+
+RouteWorkspace route_workspace(int64_t T, int64_t E) {
+    RouteWorkspace w;
+    w.nchunk = std::max<int64_t>((T + kChunk - 1) / kChunk, 1);
+    w.hist = 0;
+    w.psum = up(w.hist + 4 * (E + 1) * w.nchunk, 256);
+    w.first = up(w.psum + 4 * E * w.nchunk, 256);
+    w.psum_total = up(w.first + 4 * E, 256);
+    w.bytes = up(w.psum_total + 4 * E, 256);
+    return w;
+}
+
+int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
+    const RouteWorkspace w = route_workspace(a.T, a.E);
+    const int want_p = a.prob_sums || a.loss;
+    if (a.bf16 ? route_topk<uint16_t>(a, w, want_p, s) : route_topk<float>(a, w, want_p, s)) return 1;
+    const int E = (int)a.E;
+    uint32_t *hist = reinterpret_cast<uint32_t *>(a.ws + w.hist);
+    int32_t *first = reinterpret_cast<int32_t *>(a.ws + w.first);
+    float *psum = want_p ? reinterpret_cast<float *>(a.ws + w.psum) : nullptr;
+    float *total = want_p ? reinterpret_cast<float *>(a.ws + w.psum_total) : nullptr;
+    if (launch_dependent(route_scan_kernel, dim3(E + 1), dim3(256), 0, s, hist, (const float *)psum, w.nchunk, E,
+                         a.counts, first, total) != cudaSuccess)
+        return 1;
+    const int64_t n = a.T * a.topk;
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 1023) / 1024, (int64_t)num_sms * 8));
+    if (launch_dependent(route_place_kernel, dim3(grid), dim3(256), 0, s, (const int32_t *)a.ids, a.rows, a.T, a.topk,
+                         E, w.nchunk, (const uint32_t *)hist, (const int32_t *)a.counts, (const int32_t *)first,
+                         (const float *)total, a.coef, a.row_index, a.row_off, a.sf_row_off, a.prob_sums,
+                         a.loss) != cudaSuccess)
+        return 1;
+    return launched();
+}
+
+int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
+    return a.bf16 ? route_bwd<uint16_t>(a, num_sms, s) : route_bwd<float>(a, num_sms, s);
+}
+
+int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
+                       int64_t T, int topk, uint16_t *out, int64_t ldo, int, cudaStream_t s) {
+    combine_kernel<<<dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), 128, 0, s>>>(y, R, H, ldy, rows, weights, topk,
+                                                                                     out, ldo);
+    return launched();
+}
+
+int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y, int64_t ldy, const uint8_t *codes,
+                           const uint8_t *sf, int64_t R, int64_t H, const int32_t *rows, const float *weights,
+                           int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, int, cudaStream_t s) {
+    if (y)
+        combine_bwd_kernel<false><<<(unsigned)T, 256, 0, s>>>(dout, ldo, y, ldy, codes, sf, R, H, rows, weights, topk,
+                                                              dy, lddy, dweights);
+    else
+        combine_bwd_kernel<true><<<(unsigned)T, 256, 0, s>>>(dout, ldo, y, ldy, codes, sf, R, H, rows, weights, topk,
+                                                             dy, lddy, dweights);
+    return launched();
+}
+
+int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
+                       int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int num_sms, cudaStream_t s) {
+    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 8) + 255) / 256, (int64_t)num_sms * 16);
+    swiglu_ckpt_kernel<<<grid, 256, 0, s>>>(u, M, F, ldu, n_rows, h, ldh, codes, sf, amax);
+    return launched();
+}
+
+int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
+                           int64_t F, const int32_t *n_rows, uint16_t *du, int64_t lddu, uint16_t *h, int64_t ldh,
+                           int num_sms, cudaStream_t s) {
+    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 8) + 255) / 256, (int64_t)num_sms * 16);
+    swiglu_ckpt_bwd_kernel<<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, n_rows, du, lddu, h, ldh);
+    return launched();
+}
+
+}  // namespace bsq

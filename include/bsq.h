@@ -396,6 +396,112 @@ BSQ_API int bsq_grouped_gemm_nvfp4_out(int fmt, int G, const int32_t *row_offset
                                        uint8_t *out_sf_dev, float *out_amax_dev, void *C_bf16_dev, int64_t ldc,
                                        void *stream);
 
+/* ---- mixture-of-experts training step --------------------------------
+ * The calls between the quantizers and the grouped GEMM when such a layer
+ * is trained.  The pages describe the layer ("Thinking Machines ...",
+ * section "A precision choice for each stage": expert layers in NVFP4
+ * forward, MXFP8 backward) and not these operators; their definitions
+ * follow here.  All of them sum in fp32 in a fixed order: the same inputs
+ * give the same bits.
+ *
+ * Slots.  Each token has topk slots; slot j of token t holds an expert, the
+ * routed row the token has there, and a weight.  A slot is empty when the
+ * token is masked (token_mask_dev[t] == 0: padding) or when fewer than j + 1
+ * of its logits are above -inf; an empty slot has expert -1, row -1 and
+ * weight 0, and is counted nowhere. */
+
+/* The router.  logits [T][E] (fp32 or bf16 by logits_type, BSQ_OUT_*; leading
+ * dimension ldl in elements, any alignment of whole elements); values are
+ * finite or -inf (an expert shut to that token); a masked token's logits are
+ * not looked at and may be anything.  token_mask_dev: uint8 [T] or NULL.
+ *   experts: the topk logits of each token by (-logit, expert id), in that
+ *         order (expert_ids [T][topk]);
+ *   weights [T][topk]: renorm != 0: the softmax over the token's chosen
+ *         logits; 0: the softmax over all of them, at the chosen ones;
+ *   counts [E + 1]: slots per expert; counts[E] = tokens with a slot;
+ *   row_offsets, sf_row_offsets [E + 1]: the groups as bsq_quant_nvfp4 and
+ *         bsq_grouped_gemm take them (SF rows padded to 128 per expert);
+ *   row_index [T * topk]: the token of each routed row, by expert, then
+ *         token; the entries from row_offsets[E] on (empty slots) repeat
+ *         row_index[0] (0 when nothing is routed), so that a gather over all
+ *         T * topk rows stays in range and has the routed rows' amax;
+ *   rows [T][topk]: the routed row of each slot.  With no empty slot, rows
+ *         and weights, with offsets 0, topk, 2 topk ..., are the lists that
+ *         bsq_combine_s2f6 takes.
+ * The balance loss, when loss_dev is not NULL: with n = counts[E],
+ * f_e = counts[e] / (topk n) and prob_sums_dev[e] = sum over those n tokens
+ * of the softmax over all experts (fp32 [E], or NULL when not wanted),
+ *   *loss_dev = balance_coef E sum_e f_e prob_sums[e] / n   (0 when n = 0).
+ * workspace_dev: bsq_moe_route_workspace(T, E) bytes, 256-byte aligned, owned
+ * by the caller; scratch, so calls (and graphs) that may run at the same time
+ * need one each.  All other arrays are 4-byte aligned.  1 <= topk <= E;
+ * E > 1024, topk > 32 or T * topk + 128 E >= 2^31: BSQ_ERR_UNSUPPORTED. */
+BSQ_API size_t bsq_moe_route_workspace(int64_t T, int64_t E);
+BSQ_API int bsq_moe_route(const void *logits_dev, int logits_type, int64_t T, int64_t E, int64_t ldl,
+                          const uint8_t *token_mask_dev, int topk, int renorm, int32_t *expert_ids_dev,
+                          float *weights_dev, int32_t *rows_dev, int32_t *row_index_dev, int32_t *row_offsets_dev,
+                          int32_t *sf_row_offsets_dev, int32_t *counts_dev, float *prob_sums_dev, float balance_coef,
+                          float *loss_dev, void *workspace_dev, size_t workspace_bytes, void *stream);
+
+/* The gradient of the logits: the weights' (dweights_dev [T][topk], or NULL
+ * for none; entries of empty slots are not looked at) plus the balance
+ * loss's times *dloss_dev (NULL for none; counts_dev then may be NULL too).
+ * The loss's gradient treats counts as constants:
+ *   dlogit_te += *dloss balance_coef E / n * p_te (f_e - sum_i f_i p_ti).
+ * Given counts summed over several ranks it is the gradient of the loss over
+ * all of their tokens.  expert_ids and weights are the router's; a token
+ * without a slot gets zeros.  dlogits [T][E] has the logits' type and leading
+ * dimension ldd, and may not overlap the logits. */
+BSQ_API int bsq_moe_route_bwd(const void *logits_dev, int logits_type, int64_t T, int64_t E, int64_t ldl, int topk,
+                              int renorm, const int32_t *expert_ids_dev, const float *weights_dev,
+                              const float *dweights_dev, const int32_t *counts_dev, float balance_coef,
+                              const float *dloss_dev, void *dlogits_dev, int64_t ldd, void *stream);
+
+/* The combine of expert rows kept in bf16: out[t] = sum_j weights[t][j] *
+ * y[rows[t][j]] over slots in order, fp32, rounded once to bf16 [T][H];
+ * weights NULL means 1 (the sum of the rows' gradients that a token's input
+ * gets).  A slot whose row is outside [0, R) adds nothing; a token without
+ * slots gets zeros.  y [R][H] and out bf16; H % 8 == 0.  topk > 32 or
+ * H > 2^25: BSQ_ERR_UNSUPPORTED. */
+BSQ_API int bsq_moe_combine(const void *y_bf16, int64_t R, int64_t H, int64_t ldy, const int32_t *rows_dev,
+                            const float *weights_dev, int64_t T, int topk, void *out_bf16_dev, int64_t ldo,
+                            void *stream);
+
+/* Its gradients, from dout [T][H] (bf16): dy[rows[t][j]] = bf16(weights[t][j]
+ * * dout[t]) and dweights[t][j] = <dout[t], y[rows[t][j]]> (fp32; 0 for an
+ * empty slot).  Rows of dy that no slot lists are left as they were; a row is
+ * listed by at most one slot (the router's rows are).  y is bf16 (y_bf16,
+ * ldy), or the 8-bit form it was kept in (y_bf16 NULL): MXFP8 codes [R][H]
+ * and swizzled scales as bsq_quant_mxfp8 writes them, H % 32 == 0.  dy may
+ * not overlap the inputs. */
+BSQ_API int bsq_moe_combine_bwd(const void *dout_bf16, int64_t ldo, const void *y_bf16, int64_t ldy,
+                                const uint8_t *y_codes_dev, const uint8_t *y_sf_dev, int64_t R, int64_t H,
+                                const int32_t *rows_dev, const float *weights_dev, int64_t T, int topk,
+                                void *dy_bf16_dev, int64_t lddy, float *dweights_dev, void *stream);
+
+/* Gated SiLU with an 8-bit checkpoint.  u [M][2F] (bf16) holds the gate g in
+ * columns 0..F and v in columns F..2F:
+ *   h = bf16(g * sigmoid(g) * v)                      [M][F], fp32 inside;
+ *   codes [M][2F], sf: u in MXFP8, the bytes that bsq_quant_mxfp8(u, row-wise,
+ *         BSQ_RNE) writes -- what the backward pass keeps instead of u;
+ *   *amax_dev (if not NULL): max |h|, for bsq_quant_nvfp4(amax_in_dev) of h.
+ * n_rows_dev (int32, or NULL for M): only the first min(M, *n_rows_dev) rows
+ * exist (for instance row_offsets + E of bsq_moe_route, whose last rows are
+ * empty slots); the others are neither read nor written.  F % 32 == 0;
+ * ldu >= 2F. */
+BSQ_API int bsq_swiglu_ckpt(const void *u_bf16, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows_dev,
+                            void *h_bf16_dev, int64_t ldh, uint8_t *codes_dev, uint8_t *sf_dev, float *amax_dev,
+                            void *stream);
+
+/* Its gradient from the checkpoint (g and v are the decoded MXFP8 values) and
+ * dh [M][F] (bf16), with s = sigmoid(g): du [M][2F] (bf16) holds
+ * dh * v * s * (1 + g * (1 - s)) and dh * g * s.  h_bf16_dev, if not NULL,
+ * also receives h formed again from the checkpoint, for the weight gradient
+ * of the product that consumed it.  n_rows_dev as above. */
+BSQ_API int bsq_swiglu_ckpt_bwd(const void *dh_bf16, int64_t lddh, const uint8_t *codes_dev, const uint8_t *sf_dev,
+                                int64_t M, int64_t F, const int32_t *n_rows_dev, void *du_bf16_dev, int64_t lddu,
+                                void *h_bf16_dev, int64_t ldh, void *stream);
+
 /* Synchronize `stream`, then read and clear this device's error word.
  * Returns BSQ_OK, BSQ_ERR_TIMEOUT (a kernel's bounded wait ran out; the
  * kernel returned early and its outputs are undefined) or BSQ_ERR_CUDA. */
