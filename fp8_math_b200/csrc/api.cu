@@ -667,9 +667,16 @@ int bsq_moe_combine_bwd(const void *dout, int64_t ldo, const void *y, int64_t ld
                : BSQ_OK;
 }
 
+// The kernels number units of 16 columns in 32 bits (and no more than the
+// card's memory holds: u alone would take 2^37 bytes).
+static bool swiglu_too_large(int64_t M, int64_t F) {
+    return M >= (int64_t(1) << 31) || F >= (int64_t(1) << 31) || (F > 0 && M >= (int64_t(1) << 31) * 16 / F);
+}
+
 int bsq_swiglu_ckpt(const void *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, void *h, int64_t ldh,
                     uint8_t *codes, uint8_t *sf, float *amax, void *stream) {
     if (M < 0 || F < 0 || F % 32 || ldu < 2 * F || ldh < F) return BSQ_ERR_INVALID;
+    if (swiglu_too_large(M, F)) return BSQ_ERR_UNSUPPORTED;
     if (M > 0 && F > 0 && (!u || !h || !codes || !sf)) return BSQ_ERR_INVALID;
     if (!aligned16(u) || !aligned16(h) || !aligned16(codes) || !aligned16(sf) || ldu % 8 || ldh % 8 ||
         !aligned4(n_rows) || !aligned4(amax))
@@ -688,6 +695,7 @@ int bsq_swiglu_ckpt(const void *u, int64_t M, int64_t F, int64_t ldu, const int3
 int bsq_swiglu_ckpt_bwd(const void *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M, int64_t F,
                         const int32_t *n_rows, void *du, int64_t lddu, void *h, int64_t ldh, void *stream) {
     if (M < 0 || F < 0 || F % 32 || lddh < F || lddu < 2 * F || (h && ldh < F)) return BSQ_ERR_INVALID;
+    if (swiglu_too_large(M, F)) return BSQ_ERR_UNSUPPORTED;
     if (M > 0 && F > 0 && (!dh || !codes || !sf || !du)) return BSQ_ERR_INVALID;
     if (!aligned16(dh) || !aligned16(codes) || !aligned16(sf) || !aligned16(du) || !aligned16(h) || lddh % 8 ||
         lddu % 8 || (h && ldh % 8) || !aligned4(n_rows))

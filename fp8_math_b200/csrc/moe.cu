@@ -479,113 +479,190 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__rest
 }
 
 // ------------------------------------------------------------------ gated SiLU with an MXFP8 checkpoint
-// sigmoid(g) and its complement's product form: e = exp(-|g|) never overflows.
+// 2^x (relative error 2^-22, subnormal results kept) and 1/x (1 ulp).
+BSQ_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+BSQ_DEV float rcp(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.44269504088896341f;
+
+// sigmoid(g) as r or e r with e = exp(-|g|), r = 1 / (1 + e): e never
+// overflows and r lies in [1/2, 1].  Relative error (8 + |g|) 2^-24 at most,
+// the |g| from the rounding of the exponent; results are rounded to 2^-8.
 BSQ_DEV float sigmoid(float g) {
-    const float e = expf(-fabsf(g));
-    const float r = 1.0f / (1.0f + e);
+    const float e = ex2(-fabsf(g) * kLog2e);
+    const float r = rcp(1.0f + e);
     return g >= 0.0f ? r : e * r;
 }
 
-// Row-wise MXFP8 of eight values, four lanes per block of 32 (the bytes of
-// bsq_quant_mxfp8 with nearest rounding): returns the codes, *scale_code the
-// block's E8M0 code.
-BSQ_DEV uint2 mx_encode_quad(const float v[8], uint32_t *scale_code) {
-    float m = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[i]));
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-    if (m == 0.0f) {
-        *scale_code = 0;
-        return make_uint2(0u, 0u);  // an all-zero block has +0 codes
-    }
-    const int E = max(floor_log2(m) - 8, -127);
-    *scale_code = (uint32_t)(E + 127);
-    const float inv = exp2i(-E);
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 8; i++) s[i] = fminf(fmaxf(v[i] * inv, -448.0f), 448.0f);
-    return make_uint2(cvt_e4m3x2(s[0], s[1]) | (cvt_e4m3x2(s[2], s[3]) << 16),
-                      cvt_e4m3x2(s[4], s[5]) | (cvt_e4m3x2(s[6], s[7]) << 16));
+// n / d for the grid's 32-bit unit numbers: multiply-shift with a
+// precomputed multiplier (Granlund and Montgomery, PLDI'94).
+struct UnitDiv {
+    uint32_t d, mul, sh1, sh2;
+};
+UnitDiv unit_div(uint32_t d) {
+    int l = 0;
+    while (l < 32 && (uint64_t(1) << l) < d) l++;
+    const uint64_t m = ((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1;
+    return UnitDiv{d, (uint32_t)m, (uint32_t)std::min(l, 1), (uint32_t)std::max(l - 1, 0)};
+}
+BSQ_DEV uint32_t divide(uint32_t n, const UnitDiv &v) {
+    const uint32_t t = __umulhi(v.mul, n);
+    return (t + ((n - t) >> v.sh1)) >> v.sh2;
 }
 
+// max(|a|, |b|) of two bf16 pairs
+BSQ_DEV uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+    return r;
+}
+
+// Row-wise MXFP8 of 16 values, two lanes per block of 32 (the bytes of
+// bsq_quant_mxfp8 with nearest rounding).  The block maximum is taken on the
+// bf16 words; its exponent field minus 8 is the scale code (0 where that
+// would be below 0, and for an all-zero block, whose codes are +0), and the
+// products with 2^-E are exact.
+BSQ_DEV uint4 mx_encode16(const uint32_t w[8], uint32_t *scale_code) {
+    uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(w[0], w[1]), absmax_bf16x2(w[2], w[3])),
+                               absmax_bf16x2(absmax_bf16x2(w[4], w[5]), absmax_bf16x2(w[6], w[7])));
+    m = absmax_bf16x2(m, __shfl_xor_sync(kFull, m, 1));
+    m = max(m & 0xFFFFu, m >> 16);
+    const uint32_t sb = (uint32_t)max((int)(m >> 7) - 8, 0);
+    *scale_code = sb;
+    const float inv = __uint_as_float((254u - sb) << 23);
+    const f32x2 inv2 = f2_pack(inv, inv);
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float a, b, c, d;
+        f2_unpack(f2_mul(f2_pack(bf16_lo(w[2 * i]), bf16_hi(w[2 * i])), inv2), a, b);
+        f2_unpack(f2_mul(f2_pack(bf16_lo(w[2 * i + 1]), bf16_hi(w[2 * i + 1])), inv2), c, d);
+        q[i] = cvt_e4m3x2(a, b) | (cvt_e4m3x2(c, d) << 16);  // saturating: +-448 beyond
+    }
+    const uint32_t keep = m ? 0xFFFFFFFFu : 0u;
+    return make_uint4(q[0] & keep, q[1] & keep, q[2] & keep, q[3] & keep);
+}
+
+BSQ_DEV void load16(const uint16_t *p, uint32_t w[8]) { load_words16(p, w); }
+BSQ_DEV void store16(uint16_t *p, const uint32_t w[8]) {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// Memory bound: 8.06 bytes per h.  A thread takes 16 columns of the gate and
+// the same 16 of v (64 bytes in flight), so two lanes share a block of 32 and
+// write one scale byte each.
 __global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F,
-                                                          int64_t ldu, const int32_t *__restrict__ n_rows,
+                                                          int64_t ldu, UnitDiv per, const int32_t *__restrict__ n_rows,
                                                           uint16_t *__restrict__ h, int64_t ldh,
                                                           uint8_t *__restrict__ codes, uint8_t *__restrict__ sf,
                                                           unsigned int *__restrict__ amax) {
-    __shared__ float part[8];
+    __shared__ unsigned int part[8];
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
-    const int64_t per = F / 8, n = rows * per;
-    float top = 0.0f;
-    // n is a multiple of 4: the four lanes of a block leave the loop together; the shuffles want whole warps
-    const int64_t round = (n + 31) / 32 * 32;
+    const int64_t n = rows * per.d;  // even: a block's two lanes go together
+    uint32_t top = 0;
+    const int64_t round = (n + 31) & ~int64_t(31);  // the shuffle wants whole warps
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < round; i += (int64_t)gridDim.x * 256) {
-        const bool in = i < n;
-        const int64_t r = in ? i / per : 0, c = in ? (i - r * per) * 8 : 0;
-        float g[8], v[8];
-        load8_bf16(u + r * ldu + c, g);
-        load8_bf16(u + r * ldu + F + c, v);
+        const uint32_t unit = i < n ? (uint32_t)i : 0u;
+        const uint32_t r = divide(unit, per);
+        const int64_t c = (int64_t)(unit - r * per.d) * 16;
+        uint32_t g[8], v[8], o[8];
+        load16(u + r * ldu + c, g);
+        load16(u + r * ldu + F + c, v);
         uint32_t sg, sv;
-        const uint2 cg = mx_encode_quad(g, &sg), cv = mx_encode_quad(v, &sv);
-        if (!in) continue;
-        uint32_t o[4];
+        const uint4 cg = mx_encode16(g, &sg), cv = mx_encode16(v, &sv);
+        if (i >= n) continue;
 #pragma unroll
-        for (int q = 0; q < 4; q++) {
-            const float a = g[2 * q] * sigmoid(g[2 * q]) * v[2 * q];
-            const float b = g[2 * q + 1] * sigmoid(g[2 * q + 1]) * v[2 * q + 1];
-            o[q] = pack_bf16(a, b);
-            top = fmaxf(top, fmaxf(fabsf(bf16_lo(o[q])), fabsf(bf16_hi(o[q]))));
+        for (int q = 0; q < 8; q++) {
+            const float g0 = bf16_lo(g[q]), g1 = bf16_hi(g[q]);
+            o[q] = pack_bf16(g0 * sigmoid(g0) * bf16_lo(v[q]), g1 * sigmoid(g1) * bf16_hi(v[q]));
+            top = absmax_bf16x2(top, o[q]);
         }
-        *reinterpret_cast<uint4 *>(h + r * ldh + c) = make_uint4(o[0], o[1], o[2], o[3]);
-        *reinterpret_cast<uint2 *>(codes + r * 2 * F + c) = cg;
-        *reinterpret_cast<uint2 *>(codes + r * 2 * F + F + c) = cv;
-        if ((threadIdx.x & 3) == 0) {
-            sf[sf_offset(r, c >> 5, F >> 4)] = (uint8_t)sg;
-            sf[sf_offset(r, (F + c) >> 5, F >> 4)] = (uint8_t)sv;
-        }
+        store16(h + r * ldh + c, o);
+        uint8_t *row = codes + (int64_t)r * 2 * F + c;
+        *reinterpret_cast<uint4 *>(row) = cg;
+        *reinterpret_cast<uint4 *>(row + F) = cv;
+        const bool odd = threadIdx.x & 1;
+        sf[sf_offset(r, (c + (odd ? F : 0)) >> 5, F >> 4)] = (uint8_t)(odd ? sv : sg);
     }
     if (amax) {
-        top = warp_max(top);
+        top = max(top & 0xFFFFu, top >> 16);
+        top = __reduce_max_sync(kFull, top);
         if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
         __syncthreads();
         if (threadIdx.x == 0) {
-            for (int w = 1; w < 8; w++) top = fmaxf(top, part[w]);
-            atomicMax(amax, __float_as_uint(top));  // non-negative floats order as their bits
+            for (int w = 1; w < 8; w++) top = max(top, part[w]);
+            atomicMax(amax, top << 16);  // non-negative floats order as their bits
         }
     }
 }
 
-// From the checkpoint's g and u: du = dh g s, dg = dh u s (1 + g (1 - s)),
-// and, when h is wanted, h = g s u again.
+// 16 values of an MXFP8 row from their codes and the block's scale code.
+BSQ_DEV void mx_decode16(uint4 q, uint32_t sb, f32x2 v[8]) {
+    const float scale = exp2i((int)sb - 127);
+    const f32x2 s2 = f2_pack(scale, scale);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float a, b, c, d;
+        e4m3x2_to_f32(w[i] & 0xFFFFu, a, b);
+        e4m3x2_to_f32(w[i] >> 16, c, d);
+        v[2 * i] = f2_mul(f2_pack(a, b), s2);
+        v[2 * i + 1] = f2_mul(f2_pack(c, d), s2);
+    }
+}
+
+// From the checkpoint's g and v: du = (dh v s (1 + g (1 - s)), dh g s), and,
+// when h is wanted, h = g s v again.  Memory bound: 8.06 bytes per element of
+// dh, 10.06 with h.
+template <bool AGAIN>
 __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__restrict__ dh, int64_t lddh,
                                                               const uint8_t *__restrict__ codes,
                                                               const uint8_t *__restrict__ sf, int64_t M, int64_t F,
-                                                              const int32_t *__restrict__ n_rows,
+                                                              UnitDiv per, const int32_t *__restrict__ n_rows,
                                                               uint16_t *__restrict__ du, int64_t lddu,
                                                               uint16_t *__restrict__ h, int64_t ldh) {
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
-    const int64_t per = F / 8, n = rows * per;
+    const int64_t n = rows * per.d;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / per, c = (i - r * per) * 8;
-        float d[8], g[8], v[8], x[8], y[8], w[8];
-        load8_bf16(dh + r * lddh + c, d);
-        load8_mx(codes, sf, r, c, 2 * F, g);
-        load8_mx(codes, sf, r, F + c, 2 * F, v);
+        const uint32_t r = divide((uint32_t)i, per);
+        const int64_t c = (int64_t)((uint32_t)i - r * per.d) * 16;
+        const uint8_t *row = codes + (int64_t)r * 2 * F + c;
+        uint32_t d[8], x[8], y[8], w[8];
+        f32x2 g[8], v[8];
+        load16(dh + r * lddh + c, d);
+        const uint4 qg = __ldg(reinterpret_cast<const uint4 *>(row)), qv = __ldg(reinterpret_cast<const uint4 *>(row + F));
+        const uint32_t sg = __ldg(sf + sf_offset(r, c >> 5, F >> 4)), sv = __ldg(sf + sf_offset(r, (c + F) >> 5, F >> 4));
+        mx_decode16(qg, sg, g);
+        mx_decode16(qv, sv, v);
 #pragma unroll
         for (int q = 0; q < 8; q++) {
-            const float s = sigmoid(g[q]), gs = g[q] * s;
-            x[q] = d[q] * v[q] * s * (1.0f + g[q] * (1.0f - s));
-            y[q] = d[q] * gs;
-            w[q] = gs * v[q];
+            float gg[2], vv[2], dx[2], dy[2], again[2];
+            f2_unpack(g[q], gg[0], gg[1]);
+            f2_unpack(v[q], vv[0], vv[1]);
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float dd = e ? bf16_hi(d[q]) : bf16_lo(d[q]);
+                const float s = sigmoid(gg[e]), gs = gg[e] * s;
+                dy[e] = dd * gs;
+                // s (1 + g (1 - s)) = s + gs - gs s
+                dx[e] = dd * vv[e] * fmaf(gs, 1.0f - s, s);
+                again[e] = gs * vv[e];
+            }
+            x[q] = pack_bf16(dx[0], dx[1]);
+            y[q] = pack_bf16(dy[0], dy[1]);
+            if (AGAIN) w[q] = pack_bf16(again[0], again[1]);
         }
-        *reinterpret_cast<uint4 *>(du + r * lddu + c) =
-            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-        *reinterpret_cast<uint4 *>(du + r * lddu + F + c) =
-            make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        if (h)
-            *reinterpret_cast<uint4 *>(h + r * ldh + c) =
-                make_uint4(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]), pack_bf16(w[4], w[5]), pack_bf16(w[6], w[7]));
+        store16(du + r * lddu + c, x);
+        store16(du + r * lddu + F + c, y);
+        if (AGAIN) store16(h + r * ldh + c, w);
     }
 }
 
@@ -689,16 +766,19 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
 
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
                        int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 8) + 255) / 256, (int64_t)num_sms * 16);
-    swiglu_ckpt_kernel<<<grid, 256, 0, s>>>(u, M, F, ldu, n_rows, h, ldh, codes, sf, amax);
+    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 16) + 255) / 256, (int64_t)num_sms * 8);
+    swiglu_ckpt_kernel<<<grid, 256, 0, s>>>(u, M, F, ldu, unit_div((uint32_t)(F / 16)), n_rows, h, ldh, codes, sf,
+                                            amax);
     return launched();
 }
 
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
                            int64_t F, const int32_t *n_rows, uint16_t *du, int64_t lddu, uint16_t *h, int64_t ldh,
                            int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 8) + 255) / 256, (int64_t)num_sms * 16);
-    swiglu_ckpt_bwd_kernel<<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, n_rows, du, lddu, h, ldh);
+    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 16) + 255) / 256, (int64_t)num_sms * 8);
+    const UnitDiv per = unit_div((uint32_t)(F / 16));
+    if (h) swiglu_ckpt_bwd_kernel<true><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);
+    else swiglu_ckpt_bwd_kernel<false><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);
     return launched();
 }
 
