@@ -35,25 +35,159 @@ BSQ_DEV float load_logit(const uint16_t *p) { return __uint_as_float((uint32_t)_
 BSQ_DEV void store_logit(float *p, float v) { *p = v; }
 BSQ_DEV void store_logit(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
 
-// Unsigned keys in the order of the floats (-0 taken as +0, so that equal
-// logits have equal keys).  Key 0 marks an expert that has been taken.
-BSQ_DEV uint32_t order_key(float z) {
-    const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));
-    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+// 2^x (relative error 2^-22, subnormal results kept) and 1/x (1 ulp).
+BSQ_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
-BSQ_DEV float key_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
-constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+BSQ_DEV float rcp(float x) {
+    float y;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+BSQ_DEV float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.44269504088896341f;
+
+// n / d for the grid's 32-bit unit numbers: multiply-shift with a
+// precomputed multiplier (Granlund and Montgomery, PLDI'94).
+struct UnitDiv {
+    uint32_t d, mul, sh1, sh2;
+};
+UnitDiv unit_div(uint32_t d) {
+    int l = 0;
+    while (l < 32 && (uint64_t(1) << l) < d) l++;
+    const uint64_t m = ((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1;
+    return UnitDiv{d, (uint32_t)m, (uint32_t)std::min(l, 1), (uint32_t)std::max(l - 1, 0)};
+}
+BSQ_DEV uint32_t divide(uint32_t n, const UnitDiv &v) {
+    const uint32_t t = __umulhi(v.mul, n);
+    return (t + ((n - t) >> v.sh1)) >> v.sh2;
+}
+
+// max over the warp; NaN operands are passed over
+BSQ_DEV float warp_max_redux(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// min(a, b), NaN when one of them is NaN
+BSQ_DEV float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// exp(x[i] - top) for all i, through 2^x; -inf gives 0.
+template <int N>
+BSQ_DEV void exp_below(float x[N], float top) {
+    const f32x2 t2 = f2_pack(top, top), l2 = f2_pack(kLog2e, kLog2e);
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        f2_unpack(f2_mul(f2_sub(f2_pack(x[i], x[i + 1]), t2), l2), x[i], x[i + 1]);
+        x[i] = ex2_ftz(x[i]);
+        x[i + 1] = ex2_ftz(x[i + 1]);
+    }
+    if (N & 1) x[N - 1] = ex2_ftz((x[N - 1] - top) * kLog2e);
+}
 
 // ------------------------------------------------------------------ router
+// A lane's two best candidates of its EPL logits, and the next best once both
+// are gone: k rounds of one warp maximum each then need no second look at
+// the logits, except in the few tokens where one lane holds three of the top
+// k.  Ordered by (-logit, expert); -inf is never a candidate.
+//
+// bf16 logits leave 16 bits of an fp32 free: the expert goes there, so that
+// one float comparison orders (logit, expert) and no two are equal.  Larger
+// low bits make a positive float larger and a negative one smaller; adding 0
+// turns -0 into +0 first.  -inf with low bits is a NaN, which maxima pass
+// over (and the minimum below hands on to them).
+template <typename In, int EPL>
+struct Candidates;
+
+template <int EPL>
+struct Candidates<uint16_t, EPL> {
+    float key[EPL], m1, m2;
+    int left;
+    BSQ_DEV void init(const float z[EPL], int lane) {
+        m1 = m2 = -INFINITY;
+        left = 2;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            const uint32_t b = __float_as_uint(__fadd_rn(z[i], 0.0f));
+            key[i] = __uint_as_float(b | ((uint32_t)(i * 32 + lane) ^ (~(uint32_t)((int32_t)b >> 31) & 0xFFFFu)));
+            m2 = fmaxf(m2, min_nan(m1, key[i]));
+            m1 = fmaxf(m1, key[i]);
+        }
+    }
+    // The best candidate of the warp leaves: its logit (-inf: there is none) and expert.
+    BSQ_DEV float pop(int, int &e) {
+        const float best = warp_max_redux(m1);
+        const uint32_t b = __float_as_uint(best);
+        e = (int)((b ^ ~(uint32_t)((int32_t)b >> 31)) & 0xFFFFu);
+        if (m1 == best) {
+            m1 = m2;
+            m2 = -INFINITY;
+            if (EPL > 2 && --left <= 0)
+#pragma unroll
+                for (int i = 0; i < EPL; i++) m1 = fmaxf(m1, key[i] < best ? key[i] : -INFINITY);
+        }
+        return best > -INFINITY ? __uint_as_float(b & 0xFFFF0000u) : -INFINITY;
+    }
+};
+
+template <int EPL>
+struct Candidates<float, EPL> {
+    float z[EPL], m1, m2;
+    int e1, e2, left;
+    BSQ_DEV void init(const float x[EPL], int) {
+        m1 = m2 = -INFINITY;
+        e1 = e2 = 0;
+        left = 2;
+#pragma unroll
+        for (int i = 0; i < EPL; i++) {
+            z[i] = x[i];
+            const bool first = x[i] > m1, second = x[i] > m2;
+            e2 = first ? e1 : second ? i : e2;
+            m2 = fmaxf(m2, fminf(m1, x[i]));
+            e1 = first ? i : e1;
+            m1 = first ? x[i] : m1;
+        }
+    }
+    BSQ_DEV float pop(int lane, int &e) {
+        const float best = warp_max_redux(m1);
+        // the lowest expert among the lanes that hold this logit
+        e = (int)__reduce_min_sync(kFull, m1 == best ? (unsigned)(e1 * 32 + lane) : 0xFFFFu);
+        if (e == e1 * 32 + lane && m1 == best) {
+            const int at = e1;
+            m1 = m2;
+            e1 = e2;
+            m2 = -INFINITY;
+            if (EPL > 2 && --left <= 0) {
+#pragma unroll
+                for (int i = 0; i < EPL; i++)
+                    if ((z[i] < best || (z[i] == best && i > at)) && z[i] > m1) {
+                        m1 = z[i];
+                        e1 = i;
+                    }
+            }
+        }
+        return best;
+    }
+};
+
 // Pass 1.  A CTA takes kChunk consecutive tokens, a warp one token at a time;
-// lane l holds the logits of experts l, l + 32, ...  k rounds of "largest
-// key, then lowest expert that has it" (two warp reductions) give the top-k
-// by (-logit, expert).  A slot whose best logit is -inf stays empty.  The
-// softmax sum runs over the same registers.  The chosen experts go into one
-// 64-bit mask of tokens per expert, whose population count is the chunk's
-// count and whose bits below a token are that token's rank in the chunk:
-// the order "by expert, then token" needs no sort.  Row E of the counts is
-// the number of tokens with at least one expert.
+// lane l holds the logits of experts l, l + 32, ...  The softmax sum runs over
+// the same registers.  The chosen experts go into one 64-bit mask of tokens
+// per expert, whose population count is the chunk's count and whose bits below
+// a token are that token's rank in the chunk: the order "by expert, then
+// token" needs no sort.  Row E of the counts is the number of tokens with at
+// least one expert.
 template <typename In, int EPL>
 __global__ void __launch_bounds__(256) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                          const uint8_t *__restrict__ mask, int k, int renorm,
@@ -61,6 +195,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const In *__restrict__ 
                                                          float *__restrict__ weights, int32_t *__restrict__ rows,
                                                          int64_t nchunk, uint32_t *__restrict__ hist,
                                                          float *__restrict__ psum) {
+    grid_dependents_launch();
     extern __shared__ unsigned long long smem[];
     unsigned int *words = reinterpret_cast<unsigned int *>(smem);               // [(E + 1) * 2]
     uint16_t *sel = reinterpret_cast<uint16_t *>(words + 2 * (E + 1));          // [kChunk][k]
@@ -75,60 +210,43 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const In *__restrict__ 
     for (int tl = warp; tl < kChunk; tl += 8) {
         const int64_t t = t0 + tl;
         if (t >= T) break;
-        const bool live = !mask || __ldg(mask + t) != 0;
-        uint32_t key[EPL];
-        float z[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const int e = i * 32 + lane;
-            const bool in = live && e < E;
-            z[i] = in ? load_logit(logits + t * ldl + e) : -INFINITY;
-            key[i] = in ? order_key(z[i]) : 0u;
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < EPL; i++) top = fmaxf(top, z[i]);
-        top = warp_max(top);
-        float sum_all = 0.0f;
-        if (want_p || !renorm) {
-            const float base = top == -INFINITY ? 0.0f : top;
+        float my_z = -INFINITY, sum = 0.0f, top = 0.0f;
+        int my_e = -1;
+        if (!mask || __ldg(mask + t) != 0) {
+            float z[EPL];
 #pragma unroll
             for (int i = 0; i < EPL; i++) {
-                z[i] = expf(z[i] - base);
-                sum_all += z[i];
+                const int e = i * 32 + lane;
+                z[i] = e < E ? load_logit(logits + t * ldl + e) : -INFINITY;
             }
-            sum_all = warp_sum(sum_all);
-            const float inv = sum_all > 0.0f ? 1.0f / sum_all : 0.0f;
-            if (want_p)
+            Candidates<In, EPL> c;
+            c.init(z, lane);
+            for (int j = 0; j < k; j++) {
+                int e;
+                const float best = c.pop(lane, e);
+                if (!(best > -INFINITY)) break;
+                if (j == 0) top = best;
+                if (lane == j) {
+                    my_z = best;
+                    my_e = e;
+                }
+            }
+            if (want_p || !renorm) {
+                exp_below<EPL>(z, top);
 #pragma unroll
-                for (int i = 0; i < EPL; i++) acc[i] += z[i] * inv;
-        }
-        uint32_t my_key = 0;
-        int my_e = -1;
-        for (int j = 0; j < k; j++) {
-            uint32_t best = 0;
+                for (int i = 0; i < EPL; i++) sum += z[i];
+                sum = warp_sum(sum);
+                const float inv = sum > 0.0f ? rcp(sum) : 0.0f;
+                if (want_p)
 #pragma unroll
-            for (int i = 0; i < EPL; i++) best = max(best, key[i]);
-            best = __reduce_max_sync(kFull, best);
-            if (best <= kKeyNegInf) break;
-            unsigned int e = 0xFFFFu;
-#pragma unroll
-            for (int i = EPL - 1; i >= 0; i--)
-                if (key[i] == best) e = i * 32 + lane;
-            e = __reduce_min_sync(kFull, e);
-#pragma unroll
-            for (int i = 0; i < EPL; i++)
-                if (i * 32 + lane == (int)e) key[i] = 0;
-            if (lane == j) {
-                my_key = best;
-                my_e = (int)e;
+                    for (int i = 0; i < EPL; i++) acc[i] = fmaf(z[i], inv, acc[i]);
             }
         }
-        float x = my_e >= 0 ? expf(key_value(my_key) - top) : 0.0f;
-        const float sum = renorm ? warp_sum(x) : sum_all;
+        const float x = my_e >= 0 ? ex2_ftz((my_z - top) * kLog2e) : 0.0f;
+        if (renorm) sum = warp_sum(x);
         if (lane < k) {
             ids[t * k + lane] = my_e;
-            weights[t * k + lane] = my_e >= 0 ? x / sum : 0.0f;
+            weights[t * k + lane] = my_e >= 0 ? x * rcp(sum) : 0.0f;
             sel[tl * k + lane] = (uint16_t)my_e;
             if (my_e >= 0) atomicOr(&words[2 * my_e + (tl >> 5)], 1u << (tl & 31));
             if (lane == 0 && my_e >= 0) atomicOr(&words[2 * E + (tl >> 5)], 1u << (tl & 31));
@@ -140,16 +258,10 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const In *__restrict__ 
             if (i * 32 + lane < E) red[warp * E + i * 32 + lane] = acc[i];
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < kChunk * k; i += 256) {
-        const int tl = i / k;
-        if (t0 + tl >= T) break;
+    const int here = (int)min((int64_t)kChunk, T - t0);
+    for (int i = threadIdx.x; i < here * k; i += 256) {
         const int e = (int16_t)sel[i];
-        int rank = -1;
-        if (e >= 0) {
-            const unsigned long long below = smem[e] & ((1ull << tl) - 1ull);
-            rank = __popcll(below);
-        }
-        rows[t0 * k + i] = rank;
+        rows[t0 * k + i] = e < 0 ? -1 : __popcll(smem[e] & ((1ull << (i / k)) - 1ull));
     }
     for (int e = threadIdx.x; e <= E; e += 256) {
         const unsigned long long m = smem[e];
@@ -170,6 +282,7 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const In *__restrict__ 
 __global__ void __launch_bounds__(256) route_scan_kernel(uint32_t *__restrict__ hist, const float *__restrict__ psum,
                                                          int64_t nchunk, int E, int32_t *__restrict__ counts,
                                                          int32_t *__restrict__ first, float *__restrict__ psum_total) {
+    grid_dependents_launch();
     grid_dependency_wait();
     __shared__ int wsum[8];
     __shared__ float fsum[8];
@@ -257,7 +370,7 @@ BSQ_DEV void scan_counts(const int32_t *counts, int E, int32_t *off, int *wsum) 
 // rank inside the chunk; the rows past the last routed one repeat the first
 // row's token.  CTA 0 also writes the offsets and the loss.
 __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ rows,
-                                                          int64_t T, int k, int E, int64_t nchunk,
+                                                          uint32_t n, UnitDiv k, int E, int64_t nchunk,
                                                           const uint32_t *__restrict__ hist,
                                                           const int32_t *__restrict__ counts,
                                                           const int32_t *__restrict__ first,
@@ -275,10 +388,10 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
     for (int e = threadIdx.x; e < E; e += 256)
         if (off[e] == 0 && off[e + 1] > 0) first_token = first[e];  // one expert only
     __syncthreads();
-    const int64_t n = T * k, total = off[E];
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const uint32_t total = (uint32_t)off[E];
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {  // n < 2^31
         const int e = ids[i];
-        const int64_t t = i / k;
+        const uint32_t t = divide(i, k);
         if (e >= 0) {
             const int row = off[e] + (int)hist[(int64_t)e * nchunk + t / kChunk] + rows[i];
             rows[i] = row;
@@ -306,7 +419,7 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
                 for (int w = 0; w < 8; w++) v += fsum[w];
                 const float tokens = (float)counts[E];
                 // E / (k n^2) * sum c_e sum_t p_te, by two divisions: n^2 may pass 2^24
-                *loss = counts[E] > 0 ? coef * (float)E * (v / tokens) / ((float)k * tokens) : 0.0f;
+                *loss = counts[E] > 0 ? coef * (float)E * (v / tokens) / ((float)k.d * tokens) : 0.0f;
             }
         }
         scan_counts<true>(counts, E, off, wsum);
@@ -318,8 +431,11 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
 // One warp per token.  With q the weights' distribution (the softmax over all
 // experts, or over the chosen ones) and a_e = dL/dweight of expert e (zero
 // where it was not chosen): dz_e = q_e (a_e - sum q a).  The balance loss adds
-// the softmax's gradient of sum_e b_e p_e with b_e = dloss coef E c_e / (k n^2).
-template <typename In, int EPL>
+// the softmax's gradient of sum_e b_e p_e with b_e = dloss coef E c_e / (k n^2),
+// kept in shared memory for the CTA.  The chosen experts' own terms reach the
+// lanes that hold those experts through a row of shared memory per warp, which
+// is zero between tokens.
+template <typename In, int EPL, bool NEED_P>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                         int k, int renorm, const int32_t *__restrict__ ids,
                                                         const float *__restrict__ weights,
@@ -327,13 +443,22 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ l
                                                         const int32_t *__restrict__ counts, float coef,
                                                         const float *__restrict__ dloss, In *__restrict__ dlogits,
                                                         int64_t ldd) {
+    __shared__ float own_rows[8][EPL * 32];
+    __shared__ float bias[NEED_P ? EPL * 32 : 1];
     const int lane = threadIdx.x & 31;
-    float bscale = 0.0f;
-    if (dloss) {
-        const int n = __ldg(counts + E);
-        bscale = n > 0 ? __ldg(dloss) * coef * (float)E / (float)n / ((float)k * (float)n) : 0.0f;
+    float *own_row = own_rows[threadIdx.x >> 5];
+#pragma unroll
+    for (int i = 0; i < EPL; i++) own_row[i * 32 + lane] = 0.0f;
+    if (NEED_P) {
+        float bscale = 0.0f;
+        if (dloss) {
+            const int n = __ldg(counts + E);
+            bscale = n > 0 ? __ldg(dloss) * coef * (float)E / (float)n / ((float)k * (float)n) : 0.0f;
+        }
+        for (int e = threadIdx.x; e < EPL * 32; e += 256)
+            bias[e] = dloss && e < E ? bscale * (float)__ldg(counts + e) : 0.0f;
     }
-    const bool need_p = !renorm || dloss;
+    __syncthreads();
     const int64_t stride = (int64_t)gridDim.x * 8;
     for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += stride) {
         int e_j = -1;
@@ -346,49 +471,45 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ l
                 a_j = dweights ? __ldg(dweights + t * k + lane) : 0.0f;
             }
         }
-        const bool live = __any_sync(kFull, e_j >= 0);
-        const float dot = warp_sum(w_j * a_j);  // sum over chosen of q a: both kinds of q have q_ej = w_j
-        float d[EPL];
-#pragma unroll
-        for (int i = 0; i < EPL; i++) d[i] = 0.0f;
-        if (live && need_p) {
-            float p[EPL], top = -INFINITY;
+        float p[EPL];
+        const bool live = __any_sync(kFull, e_j >= 0);  // a masked token's logits are not read
+        if (NEED_P && live) {
 #pragma unroll
             for (int i = 0; i < EPL; i++) {
                 const int e = i * 32 + lane;
                 p[i] = e < E ? load_logit(logits + t * ldl + e) : -INFINITY;
-                top = fmaxf(top, p[i]);
             }
-            top = warp_max(top);
+        }
+        const float dot = warp_sum(w_j * a_j);  // sum over chosen of q a: both kinds of q have q_ej = w_j
+        // the chosen experts' own term: w_j (a_j - dot), or w_j a_j where dot goes over all experts
+        if (e_j >= 0) own_row[e_j] = renorm ? w_j * (a_j - dot) : w_j * a_j;
+        float d[EPL];
+        if (NEED_P && live) {
+            float top = p[0];
+#pragma unroll
+            for (int i = 1; i < EPL; i++) top = fmaxf(top, p[i]);
+            top = warp_max_redux(top);
+            exp_below<EPL>(p, top);
             float s = 0.0f, pb = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPL; i++) {
-                p[i] = expf(p[i] - top);
+                d[i] = bias[i * 32 + lane];
                 s += p[i];
+                pb = fmaf(p[i], d[i], pb);
             }
-            const float inv = 1.0f / warp_sum(s);
-            float b[EPL];
+            const float inv = rcp(warp_sum(s));
+            const float sub = warp_sum(pb) * inv + (renorm ? 0.0f : dot);
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < EPL; i++) {
-                const int e = i * 32 + lane;
-                p[i] *= inv;
-                b[i] = dloss && e < E ? bscale * (float)__ldg(counts + e) : 0.0f;
-                pb += p[i] * b[i];
-            }
-            pb = warp_sum(pb);
-            const float sub = pb + (renorm ? 0.0f : dot);
+            for (int i = 0; i < EPL; i++) d[i] = fmaf(p[i] * inv, d[i] - sub, own_row[i * 32 + lane]);
+        } else {
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < EPL; i++) d[i] = p[i] * (b[i] - sub);
+            for (int i = 0; i < EPL; i++) d[i] = own_row[i * 32 + lane];
         }
-        // the chosen experts' own term: w_j (a_j - dot), or w_j a_j where dot went over all experts
-        const float own = renorm ? w_j * (a_j - dot) : w_j * a_j;
-        for (int j = 0; j < k; j++) {
-            const int e = __shfl_sync(kFull, e_j, j);
-            const float v = __shfl_sync(kFull, own, j);
-#pragma unroll
-            for (int i = 0; i < EPL; i++)
-                if (i * 32 + lane == e) d[i] += v;
-        }
+        __syncwarp();
+        if (e_j >= 0) own_row[e_j] = 0.0f;
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < EPL; i++)
             if (i * 32 + lane < E) store_logit(dlogits + t * ldd + i * 32 + lane, d[i]);
@@ -479,19 +600,6 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__rest
 }
 
 // ------------------------------------------------------------------ gated SiLU with an MXFP8 checkpoint
-// 2^x (relative error 2^-22, subnormal results kept) and 1/x (1 ulp).
-BSQ_DEV float ex2(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-BSQ_DEV float rcp(float x) {
-    float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-constexpr float kLog2e = 1.44269504088896341f;
-
 // sigmoid(g) as r or e r with e = exp(-|g|), r = 1 / (1 + e): e never
 // overflows and r lies in [1/2, 1].  Relative error (8 + |g|) 2^-24 at most,
 // the |g| from the rounding of the exponent; results are rounded to 2^-8.
@@ -499,22 +607,6 @@ BSQ_DEV float sigmoid(float g) {
     const float e = ex2(-fabsf(g) * kLog2e);
     const float r = rcp(1.0f + e);
     return g >= 0.0f ? r : e * r;
-}
-
-// n / d for the grid's 32-bit unit numbers: multiply-shift with a
-// precomputed multiplier (Granlund and Montgomery, PLDI'94).
-struct UnitDiv {
-    uint32_t d, mul, sh1, sh2;
-};
-UnitDiv unit_div(uint32_t d) {
-    int l = 0;
-    while (l < 32 && (uint64_t(1) << l) < d) l++;
-    const uint64_t m = ((uint64_t(1) << 32) * ((uint64_t(1) << l) - d)) / d + 1;
-    return UnitDiv{d, (uint32_t)m, (uint32_t)std::min(l, 1), (uint32_t)std::max(l - 1, 0)};
-}
-BSQ_DEV uint32_t divide(uint32_t n, const UnitDiv &v) {
-    const uint32_t t = __umulhi(v.mul, n);
-    return (t + ((n - t) >> v.sh1)) >> v.sh2;
 }
 
 // max(|a|, |b|) of two bf16 pairs
@@ -683,27 +775,33 @@ int route_topk(const RouteArgs &a, const RouteWorkspace &w, int want_p, cudaStre
     };
     if (E <= 32) return run(route_topk_kernel<In, 1>);
     if (E <= 64) return run(route_topk_kernel<In, 2>);
+    if (E <= 96) return run(route_topk_kernel<In, 3>);
     if (E <= 128) return run(route_topk_kernel<In, 4>);
+    if (E <= 192) return run(route_topk_kernel<In, 6>);
     if (E <= 256) return run(route_topk_kernel<In, 8>);
+    if (E <= 384) return run(route_topk_kernel<In, 12>);
     if (E <= 512) return run(route_topk_kernel<In, 16>);
     return run(route_topk_kernel<In, 32>);
 }
 
-template <typename In>
+template <typename In, bool NEED_P>
 int route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((a.T + 7) / 8, (int64_t)num_sms * 16);
+    const unsigned grid = (unsigned)std::min<int64_t>((a.T + 7) / 8, (int64_t)num_sms * 8);
     auto run = [&](auto kern) {
         kern<<<grid, 256, 0, s>>>(static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, a.topk, a.renorm, a.ids,
                                   a.weights, a.dweights, a.counts, a.coef, a.dloss, static_cast<In *>(a.dlogits),
                                   a.ldd);
         return launched();
     };
-    if (a.E <= 32) return run(route_bwd_kernel<In, 1>);
-    if (a.E <= 64) return run(route_bwd_kernel<In, 2>);
-    if (a.E <= 128) return run(route_bwd_kernel<In, 4>);
-    if (a.E <= 256) return run(route_bwd_kernel<In, 8>);
-    if (a.E <= 512) return run(route_bwd_kernel<In, 16>);
-    return run(route_bwd_kernel<In, 32>);
+    if (a.E <= 32) return run(route_bwd_kernel<In, 1, NEED_P>);
+    if (a.E <= 64) return run(route_bwd_kernel<In, 2, NEED_P>);
+    if (a.E <= 96) return run(route_bwd_kernel<In, 3, NEED_P>);
+    if (a.E <= 128) return run(route_bwd_kernel<In, 4, NEED_P>);
+    if (a.E <= 192) return run(route_bwd_kernel<In, 6, NEED_P>);
+    if (a.E <= 256) return run(route_bwd_kernel<In, 8, NEED_P>);
+    if (a.E <= 384) return run(route_bwd_kernel<In, 12, NEED_P>);
+    if (a.E <= 512) return run(route_bwd_kernel<In, 16, NEED_P>);
+    return run(route_bwd_kernel<In, 32, NEED_P>);
 }
 
 }  // namespace
@@ -733,8 +831,8 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
         return 1;
     const int64_t n = a.T * a.topk;
     const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 1023) / 1024, (int64_t)num_sms * 8));
-    if (launch_dependent(route_place_kernel, dim3(grid), dim3(256), 0, s, (const int32_t *)a.ids, a.rows, a.T, a.topk,
-                         E, w.nchunk, (const uint32_t *)hist, (const int32_t *)a.counts, (const int32_t *)first,
+    if (launch_dependent(route_place_kernel, dim3(grid), dim3(256), 0, s, (const int32_t *)a.ids, a.rows, (uint32_t)n,
+                         unit_div((uint32_t)a.topk), E, w.nchunk, (const uint32_t *)hist, (const int32_t *)a.counts, (const int32_t *)first,
                          (const float *)total, a.coef, a.row_index, a.row_off, a.sf_row_off, a.prob_sums,
                          a.loss) != cudaSuccess)
         return 1;
@@ -742,7 +840,10 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
 }
 
 int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
-    return a.bf16 ? route_bwd<uint16_t>(a, num_sms, s) : route_bwd<float>(a, num_sms, s);
+    // the softmax over the chosen experts alone needs their weights, not the logits
+    if (!a.renorm || a.dloss)
+        return a.bf16 ? route_bwd<uint16_t, true>(a, num_sms, s) : route_bwd<float, true>(a, num_sms, s);
+    return a.bf16 ? route_bwd<uint16_t, false>(a, num_sms, s) : route_bwd<float, false>(a, num_sms, s);
 }
 
 int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
