@@ -69,13 +69,6 @@ BSQ_DEV uint32_t divide(uint32_t n, const UnitDiv &v) {
     return (t + ((n - t) >> v.sh1)) >> v.sh2;
 }
 
-// max over the warp; NaN operands are passed over
-BSQ_DEV float warp_max_redux(float v) {
-    float r;
-    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // min(a, b), NaN when one of them is NaN
 BSQ_DEV float min_nan(float a, float b) {
     float r;
@@ -83,195 +76,398 @@ BSQ_DEV float min_nan(float a, float b) {
     return r;
 }
 
-// exp(x[i] - top) for all i, through 2^x; -inf gives 0.
-template <int N>
-BSQ_DEV void exp_below(float x[N], float top) {
-    const f32x2 t2 = f2_pack(top, top), l2 = f2_pack(kLog2e, kLog2e);
+// Sum and maximum over the LPT neighbouring lanes that share a token.
+template <int LPT>
+BSQ_DEV float group_sum(float v) {
 #pragma unroll
-    for (int i = 0; i + 1 < N; i += 2) {
-        f2_unpack(f2_mul(f2_sub(f2_pack(x[i], x[i + 1]), t2), l2), x[i], x[i + 1]);
+    for (int o = LPT / 2; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+template <int LPT>
+BSQ_DEV float group_max(float v) {
+#pragma unroll
+    for (int o = LPT / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+// A lane's logits of one token: LPT lanes hold a row in quads of four
+// consecutive experts, lane `sub` the quads sub, sub + LPT, ...  Experts past
+// E are -inf.  `vec`: E % 4 == 0 and every row starts on a quad's alignment.
+template <typename In, int LPT, int Q>
+struct Row;
+
+template <int LPT, int Q>
+struct Row<uint16_t, LPT, Q> {
+    uint2 w[Q];
+    BSQ_DEV void load(const uint16_t *row, int E, int sub, bool vec, bool live) {
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            const int e = 4 * (q * LPT + sub);
+            w[q] = make_uint2(0xFF80FF80u, 0xFF80FF80u);
+            if (!live || e >= E) continue;
+            if (vec) {
+                w[q] = __ldg(reinterpret_cast<const uint2 *>(row + e));
+            } else {
+                uint32_t v[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[i] = e + i < E ? (uint32_t)__ldg(row + e + i) : 0xFF80u;
+                w[q] = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
+            }
+        }
+    }
+    BSQ_DEV void get(int q, float z[4]) const {
+        z[0] = bf16_lo(w[q].x);
+        z[1] = bf16_hi(w[q].x);
+        z[2] = bf16_lo(w[q].y);
+        z[3] = bf16_hi(w[q].y);
+    }
+};
+
+template <int LPT, int Q>
+struct Row<float, LPT, Q> {
+    float4 w[Q];
+    BSQ_DEV void load(const float *row, int E, int sub, bool vec, bool live) {
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            const int e = 4 * (q * LPT + sub);
+            w[q] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (!live || e >= E) continue;
+            if (vec) {
+                w[q] = __ldg(reinterpret_cast<const float4 *>(row + e));
+            } else {
+                w[q].x = __ldg(row + e);
+                if (e + 1 < E) w[q].y = __ldg(row + e + 1);
+                if (e + 2 < E) w[q].z = __ldg(row + e + 2);
+                if (e + 3 < E) w[q].w = __ldg(row + e + 3);
+            }
+        }
+    }
+    BSQ_DEV void get(int q, float z[4]) const {
+        z[0] = w[q].x;
+        z[1] = w[q].y;
+        z[2] = w[q].z;
+        z[3] = w[q].w;
+    }
+};
+
+// exp(x[i] - top), through 2^x; -inf gives 0.
+BSQ_DEV void exp_below4(float x[4], f32x2 top2) {
+    const f32x2 l2 = f2_pack(kLog2e, kLog2e);
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        f2_unpack(f2_mul(f2_sub(f2_pack(x[i], x[i + 1]), top2), l2), x[i], x[i + 1]);
         x[i] = ex2_ftz(x[i]);
         x[i + 1] = ex2_ftz(x[i + 1]);
     }
-    if (N & 1) x[N - 1] = ex2_ftz((x[N - 1] - top) * kLog2e);
 }
 
 // ------------------------------------------------------------------ router
-// A lane's two best candidates of its EPL logits, and the next best once both
-// are gone: k rounds of one warp maximum each then need no second look at
-// the logits, except in the few tokens where one lane holds three of the top
-// k.  Ordered by (-logit, expert); -inf is never a candidate.
+// A lane's best D candidates among its logits, in the order (-logit, expert),
+// so that each of the k rounds is one maximum over the token's lanes; a lane
+// that has given all D looks at its logits again.  D is chosen so that with k
+// near 8 few tokens need that: the lanes give k / LPT each on average.  -inf
+// is never a candidate.
 //
 // bf16 logits leave 16 bits of an fp32 free: the expert goes there, so that
 // one float comparison orders (logit, expert) and no two are equal.  Larger
 // low bits make a positive float larger and a negative one smaller; adding 0
 // turns -0 into +0 first.  -inf with low bits is a NaN, which maxima pass
-// over (and the minimum below hands on to them).
-template <typename In, int EPL>
+// over (and min_nan hands on to them).
+template <typename In, int LPT, int Q>
 struct Candidates;
 
-template <int EPL>
-struct Candidates<uint16_t, EPL> {
-    float key[EPL], m1, m2;
+template <int LPT>
+constexpr int kDepth = LPT == 8 ? 4 : LPT == 16 ? 3 : 2;
+
+template <int LPT, int Q>
+struct Candidates<uint16_t, LPT, Q> {
+    static constexpr int D = kDepth<LPT>;
+    float m[D];
     int left;
-    BSQ_DEV void init(const float z[EPL], int lane) {
-        m1 = m2 = -INFINITY;
-        left = 2;
+    template <bool AGAIN>
+    BSQ_DEV void fill(const Row<uint16_t, LPT, Q> &row, int sub, float limit) {
+        left = D;
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            const uint32_t b = __float_as_uint(__fadd_rn(z[i], 0.0f));
-            key[i] = __uint_as_float(b | ((uint32_t)(i * 32 + lane) ^ (~(uint32_t)((int32_t)b >> 31) & 0xFFFFu)));
-            m2 = fmaxf(m2, min_nan(m1, key[i]));
-            m1 = fmaxf(m1, key[i]);
+        for (int d = 0; d < D; d++) m[d] = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            float z[4];
+            row.get(q, z);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint32_t b = __float_as_uint(__fadd_rn(z[i], 0.0f));
+                const uint32_t e = (uint32_t)(4 * (q * LPT + sub) + i);
+                float key = __uint_as_float(b | (e ^ (~(uint32_t)((int32_t)b >> 31) & 0xFFFFu)));
+                if (AGAIN) key = key < limit ? key : -INFINITY;
+#pragma unroll
+                for (int d = D - 1; d > 0; d--) m[d] = fmaxf(m[d], min_nan(m[d - 1], key));
+                m[0] = fmaxf(m[0], key);
+            }
         }
     }
-    // The best candidate of the warp leaves: its logit (-inf: there is none) and expert.
-    BSQ_DEV float pop(int, int &e) {
-        const float best = warp_max_redux(m1);
+    // The best candidate of the token's lanes leaves: its logit (-inf: there is none) and expert.
+    BSQ_DEV float pop(const Row<uint16_t, LPT, Q> &row, int sub, int &e) {
+        const float best = group_max<LPT>(m[0]);
         const uint32_t b = __float_as_uint(best);
         e = (int)((b ^ ~(uint32_t)((int32_t)b >> 31)) & 0xFFFFu);
-        if (m1 == best) {
-            m1 = m2;
-            m2 = -INFINITY;
-            if (EPL > 2 && --left <= 0)
+        if (!(best > -INFINITY)) return -INFINITY;
+        if (m[0] == best) {
 #pragma unroll
-                for (int i = 0; i < EPL; i++) m1 = fmaxf(m1, key[i] < best ? key[i] : -INFINITY);
+            for (int d = 0; d + 1 < D; d++) m[d] = m[d + 1];
+            m[D - 1] = -INFINITY;
+            if (4 * Q > D && --left == 0) fill<true>(row, sub, best);
         }
-        return best > -INFINITY ? __uint_as_float(b & 0xFFFF0000u) : -INFINITY;
+        return __uint_as_float(b & 0xFFFF0000u);
     }
 };
 
-template <int EPL>
-struct Candidates<float, EPL> {
-    float z[EPL], m1, m2;
-    int e1, e2, left;
-    BSQ_DEV void init(const float x[EPL], int) {
-        m1 = m2 = -INFINITY;
-        e1 = e2 = 0;
-        left = 2;
+template <int LPT, int Q>
+struct Candidates<float, LPT, Q> {
+    static constexpr int D = kDepth<LPT>;
+    float m[D];
+    int at[D], left;
+    template <bool AGAIN>
+    BSQ_DEV void fill(const Row<float, LPT, Q> &row, int sub, float limit, int limit_e = 0) {
+        left = D;
 #pragma unroll
-        for (int i = 0; i < EPL; i++) {
-            z[i] = x[i];
-            const bool first = x[i] > m1, second = x[i] > m2;
-            e2 = first ? e1 : second ? i : e2;
-            m2 = fmaxf(m2, fminf(m1, x[i]));
-            e1 = first ? i : e1;
-            m1 = first ? x[i] : m1;
+        for (int d = 0; d < D; d++) {
+            m[d] = -INFINITY;
+            at[d] = 0xFFFF;
+        }
+#pragma unroll
+        for (int q = 0; q < Q; q++) {
+            float z[4];
+            row.get(q, z);
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int e = 4 * (q * LPT + sub) + i;
+                float x = z[i];
+                if (AGAIN) x = x < limit || (x == limit && e > limit_e) ? x : -INFINITY;
+                // a lane's experts come in rising order: equal logits stay behind the earlier one
+#pragma unroll
+                for (int d = D - 1; d > 0; d--) {
+                    at[d] = x > m[d - 1] ? at[d - 1] : x > m[d] ? e : at[d];
+                    m[d] = fmaxf(m[d], min_nan(m[d - 1], x));
+                }
+                at[0] = x > m[0] ? e : at[0];
+                m[0] = fmaxf(m[0], x);
+            }
         }
     }
-    BSQ_DEV float pop(int lane, int &e) {
-        const float best = warp_max_redux(m1);
+    BSQ_DEV float pop(const Row<float, LPT, Q> &row, int sub, int &e) {
+        const float best = group_max<LPT>(m[0]);
         // the lowest expert among the lanes that hold this logit
-        e = (int)__reduce_min_sync(kFull, m1 == best ? (unsigned)(e1 * 32 + lane) : 0xFFFFu);
-        if (e == e1 * 32 + lane && m1 == best) {
-            const int at = e1;
-            m1 = m2;
-            e1 = e2;
-            m2 = -INFINITY;
-            if (EPL > 2 && --left <= 0) {
+        int cand = m[0] == best ? at[0] : 0xFFFF;
 #pragma unroll
-                for (int i = 0; i < EPL; i++)
-                    if ((z[i] < best || (z[i] == best && i > at)) && z[i] > m1) {
-                        m1 = z[i];
-                        e1 = i;
-                    }
+        for (int o = LPT / 2; o; o >>= 1) cand = min(cand, __shfl_xor_sync(kFull, cand, o));
+        e = cand;
+        if (!(best > -INFINITY)) return -INFINITY;
+        if (m[0] == best && at[0] == cand) {
+#pragma unroll
+            for (int d = 0; d + 1 < D; d++) {
+                m[d] = m[d + 1];
+                at[d] = at[d + 1];
             }
+            m[D - 1] = -INFINITY;
+            if (4 * Q > D && --left == 0) fill<true>(row, sub, best, cand);
         }
         return best;
     }
 };
 
-// Pass 1.  A CTA takes kChunk consecutive tokens, a warp one token at a time;
-// lane l holds the logits of experts l, l + 32, ...  The softmax sum runs over
-// the same registers.  The chosen experts go into one 64-bit mask of tokens
-// per expert, whose population count is the chunk's count and whose bits below
-// a token are that token's rank in the chunk: the order "by expert, then
-// token" needs no sort.  Row E of the counts is the number of tokens with at
-// least one expert.
-template <typename In, int EPL>
-__global__ void __launch_bounds__(256) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
-                                                         const uint8_t *__restrict__ mask, int k, int renorm,
-                                                         int want_p, int32_t *__restrict__ ids,
-                                                         float *__restrict__ weights, int32_t *__restrict__ rows,
-                                                         int64_t nchunk, uint32_t *__restrict__ hist,
-                                                         float *__restrict__ psum) {
+// Exclusive scan of n[0..E) (PAD128: each rounded up to 128) into off[0..E]
+// by the CTA's first warp, 32 consecutive experts at a time.
+template <bool PAD128, class Count>
+BSQ_DEV void warp_scan(Count n, int E, int32_t *off) {
+    const int lane = threadIdx.x & 31;
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + lane;
+        int v = e < E ? n(e) : 0;
+        if (PAD128) v = (v + 127) & ~127;
+        int s = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, s, o);
+            if (lane >= o) s += u;
+        }
+        if (e < E) off[e] = carry + s - v;
+        carry += __shfl_sync(kFull, s, 31);
+    }
+    if (lane == 0) off[E] = carry;
+}
+
+// coef E / (k n^2) sum_e c_e sum_t p_te, by divisions of fp32 size.
+BSQ_DEV float balance_loss(float weighted, int tokens, float coef, int E, int k) {
+    return tokens > 0 ? coef * (float)E * (weighted / (float)tokens) / ((float)k * (float)tokens) : 0.0f;
+}
+
+struct RouteOut {
+    int32_t *ids;
+    float *weights;
+    int32_t *rows, *row_index, *row_off, *sf_row_off, *counts;
+    float *prob_sums, *loss;
+};
+
+// Pass 1.  A CTA takes kChunk consecutive tokens, LPT lanes a token.  The
+// softmax sum runs over the same registers as the choice.  The chosen experts
+// go into one 64-bit mask of tokens per expert, whose population count is the
+// chunk's count and whose bits below a token are that token's rank in the
+// chunk: the order "by expert, then token" needs no sort.  Row E of the counts
+// is the number of tokens with at least one expert.  SINGLE: the chunk is all
+// there is, and the CTA finishes the call (offsets, rows, loss).
+template <typename In, int LPT, int Q, bool SINGLE>
+__global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
+                                                         int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
+                                                         int renorm, int want_p, RouteOut out, int64_t nchunk,
+                                                         uint32_t *__restrict__ hist, float *__restrict__ psum,
+                                                         float coef) {
     grid_dependents_launch();
     extern __shared__ unsigned long long smem[];
-    unsigned int *words = reinterpret_cast<unsigned int *>(smem);               // [(E + 1) * 2]
-    uint16_t *sel = reinterpret_cast<uint16_t *>(words + 2 * (E + 1));          // [kChunk][k]
-    float *red = reinterpret_cast<float *>(sel + kChunk * k);                   // [8][E] when want_p
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < 2 * (E + 1); i += 256) words[i] = 0;
+    const int k = (int)kd.d, nwarps = blockDim.x >> 5;
+    unsigned int *words = reinterpret_cast<unsigned int *>(smem);      // [(E + 1) * 2]
+    float *sel_x = reinterpret_cast<float *>(words + 2 * (E + 1));     // [kChunk][k] exp(logit - top)
+    float *inv = sel_x + kChunk * k;                                   // [kChunk]
+    float *red = inv + kChunk;                                         // [nwarps][E] when want_p
+    int32_t *off = reinterpret_cast<int32_t *>(red + (want_p ? nwarps * E : 0));  // [E + 1] when SINGLE
+    uint16_t *sel = reinterpret_cast<uint16_t *>(off + (SINGLE ? E + 1 : 0));     // [kChunk][k]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPT;
+    constexpr int kGroups = 32 / LPT;
+    for (int i = threadIdx.x; i < 2 * (E + 1); i += blockDim.x) words[i] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * kChunk;
-    float acc[EPL];
+    const int here = (int)min((int64_t)kChunk, T - t0);
+    float acc[Q][4];
 #pragma unroll
-    for (int i = 0; i < EPL; i++) acc[i] = 0.0f;
-    for (int tl = warp; tl < kChunk; tl += 8) {
-        const int64_t t = t0 + tl;
-        if (t >= T) break;
-        float my_z = -INFINITY, sum = 0.0f, top = 0.0f;
-        int my_e = -1;
-        if (!mask || __ldg(mask + t) != 0) {
-            float z[EPL];
+    for (int q = 0; q < Q; q++)
 #pragma unroll
-            for (int i = 0; i < EPL; i++) {
-                const int e = i * 32 + lane;
-                z[i] = e < E ? load_logit(logits + t * ldl + e) : -INFINITY;
-            }
-            Candidates<In, EPL> c;
-            c.init(z, lane);
-            for (int j = 0; j < k; j++) {
+        for (int i = 0; i < 4; i++) acc[q][i] = 0.0f;
+    for (int w0 = warp * kGroups; w0 < here; w0 += nwarps * kGroups) {
+        const int tl = w0 + lane / LPT;
+        const bool in = tl < here;
+        const bool live = in && (!mask || __ldg(mask + t0 + tl) != 0);
+        Row<In, LPT, Q> row;
+        row.load(logits + (t0 + tl) * ldl, E, sub, vec, live);
+        Candidates<In, LPT, Q> c;
+        c.template fill<false>(row, sub, 0.0f);
+        float top = 0.0f, chosen = 0.0f;
+        for (int j0 = 0; j0 < k; j0 += LPT) {
+            int my_e = -1;
+            float my_x = 0.0f;
+            for (int j = j0; j < min(k, j0 + LPT); j++) {
                 int e;
-                const float best = c.pop(lane, e);
-                if (!(best > -INFINITY)) break;
-                if (j == 0) top = best;
-                if (lane == j) {
-                    my_z = best;
+                const float z = c.pop(row, sub, e);
+                const bool ok = z > -INFINITY;
+                if (j == 0 && ok) top = z;
+                const float x = ok ? ex2_ftz((z - top) * kLog2e) : 0.0f;
+                chosen += x;
+                if (ok && sub == j - j0) {
                     my_e = e;
+                    my_x = x;
                 }
             }
-            if (want_p || !renorm) {
-                exp_below<EPL>(z, top);
-#pragma unroll
-                for (int i = 0; i < EPL; i++) sum += z[i];
-                sum = warp_sum(sum);
-                const float inv = sum > 0.0f ? rcp(sum) : 0.0f;
-                if (want_p)
-#pragma unroll
-                    for (int i = 0; i < EPL; i++) acc[i] = fmaf(z[i], inv, acc[i]);
+            // a lane per slot
+            const int j = j0 + sub;
+            if (in && j < k) {
+                sel[tl * k + j] = (uint16_t)my_e;
+                sel_x[tl * k + j] = my_x;
+                if (my_e >= 0) {
+                    atomicOr(&words[2 * my_e + (tl >> 5)], 1u << (tl & 31));
+                    if (j == 0) atomicOr(&words[2 * E + (tl >> 5)], 1u << (tl & 31));
+                }
             }
         }
-        const float x = my_e >= 0 ? ex2_ftz((my_z - top) * kLog2e) : 0.0f;
-        if (renorm) sum = warp_sum(x);
-        if (lane < k) {
-            ids[t * k + lane] = my_e;
-            weights[t * k + lane] = my_e >= 0 ? x * rcp(sum) : 0.0f;
-            sel[tl * k + lane] = (uint16_t)my_e;
-            if (my_e >= 0) atomicOr(&words[2 * my_e + (tl >> 5)], 1u << (tl & 31));
-            if (lane == 0 && my_e >= 0) atomicOr(&words[2 * E + (tl >> 5)], 1u << (tl & 31));
+        if (want_p || !renorm) {
+            const f32x2 top2 = f2_pack(top, top);
+            float s = 0.0f;
+            float p[Q][4];
+#pragma unroll
+            for (int q = 0; q < Q; q++) {
+                row.get(q, p[q]);
+                exp_below4(p[q], top2);
+                s += (p[q][0] + p[q][1]) + (p[q][2] + p[q][3]);
+            }
+            s = group_sum<LPT>(s);
+            const float r = s > 0.0f ? rcp(s) : 0.0f;
+            if (want_p)
+#pragma unroll
+                for (int q = 0; q < Q; q++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) acc[q][i] = fmaf(p[q][i], r, acc[q][i]);
+            if (!renorm) chosen = s;
         }
+        if (in && sub == 0) inv[tl] = chosen > 0.0f ? rcp(chosen) : 0.0f;
     }
     if (want_p) {
 #pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (i * 32 + lane < E) red[warp * E + i * 32 + lane] = acc[i];
+        for (int q = 0; q < Q; q++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                float v = acc[q][i];
+#pragma unroll
+                for (int o = LPT; o < 32; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+                const int e = 4 * (q * LPT + sub) + i;
+                if (lane < LPT && e < E) red[warp * E + e] = v;
+            }
     }
     __syncthreads();
-    const int here = (int)min((int64_t)kChunk, T - t0);
-    for (int i = threadIdx.x; i < here * k; i += 256) {
-        const int e = (int16_t)sel[i];
-        rows[t0 * k + i] = e < 0 ? -1 : __popcll(smem[e] & ((1ull << (i / k)) - 1ull));
+    if (SINGLE) {
+        if (warp == 0) warp_scan<false>([&](int e) { return __popcll(smem[e]); }, E, off);
+        __syncthreads();
     }
-    for (int e = threadIdx.x; e <= E; e += 256) {
-        const unsigned long long m = smem[e];
-        // count in the low byte, the chunk's first token of the expert above it
-        hist[(int64_t)e * nchunk + blockIdx.x] = (uint32_t)__popcll(m) | (m ? (uint32_t)(__ffsll(m) - 1) << 8 : 0u);
-        if (want_p && e < E) {
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 8; w++) v += red[w * E + e];
-            psum[(int64_t)e * nchunk + blockIdx.x] = v;
+    for (int i = threadIdx.x; i < here * k; i += blockDim.x) {
+        const int tl = (int)divide((uint32_t)i, kd);
+        const int e = (int16_t)sel[i];
+        int row = e < 0 ? -1 : __popcll(smem[e] & ((1ull << tl) - 1ull));
+        if (SINGLE && e >= 0) {
+            row += off[e];
+            out.row_index[row] = tl;
+        }
+        out.ids[t0 * k + i] = e;
+        out.weights[t0 * k + i] = sel_x[i] * inv[tl];
+        out.rows[t0 * k + i] = row;
+    }
+    if (!SINGLE) {
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+            const unsigned long long m = smem[e];
+            // count in the low byte, the chunk's first token of the expert above it
+            hist[(int64_t)e * nchunk + blockIdx.x] =
+                (uint32_t)__popcll(m) | (m ? (uint32_t)(__ffsll(m) - 1) << 8 : 0u);
+            if (want_p && e < E) {
+                float v = 0.0f;
+                for (int w = 0; w < nwarps; w++) v += red[w * E + e];
+                psum[(int64_t)e * nchunk + blockIdx.x] = v;
+            }
+        }
+    } else {
+        const int total = off[E], tokens = __popcll(smem[E]);
+        for (int e = threadIdx.x; e < E; e += blockDim.x) {
+            if (off[e] == 0 && off[e + 1] > 0)  // the expert of the first row, and its first token
+                for (int i = total; i < here * k; i++) out.row_index[i] = __ffsll(smem[e]) - 1;
+            if (total == 0 && e == 0)
+                for (int i = 0; i < here * k; i++) out.row_index[i] = 0;
+            if (want_p) {
+                float v = 0.0f;
+                for (int w = 0; w < nwarps; w++) v += red[w * E + e];
+                red[e] = v;  // this thread's own column
+                if (out.prob_sums) out.prob_sums[e] = v;
+            }
+            out.counts[e] = off[e + 1] - off[e];
+            out.row_off[e] = off[e];
+        }
+        if (threadIdx.x == 0) {
+            out.counts[E] = tokens;
+            out.row_off[E] = total;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            if (out.loss) {
+                float v = 0.0f;
+                for (int e = lane; e < E; e += 32) v += (float)__popcll(smem[e]) * red[e];
+                v = warp_sum(v);
+                if (lane == 0) *out.loss = balance_loss(v, tokens, coef, E, k);
+            }
+            warp_scan<true>([&](int e) { return __popcll(smem[e]); }, E, out.sf_row_off);
         }
     }
 }
@@ -417,9 +613,7 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
             if (threadIdx.x == 0) {
                 float v = 0.0f;
                 for (int w = 0; w < 8; w++) v += fsum[w];
-                const float tokens = (float)counts[E];
-                // E / (k n^2) * sum c_e sum_t p_te, by two divisions: n^2 may pass 2^24
-                *loss = counts[E] > 0 ? coef * (float)E * (v / tokens) / ((float)k.d * tokens) : 0.0f;
+                *loss = balance_loss(v, counts[E], coef, E, (int)k.d);
             }
         }
         scan_counts<true>(counts, E, off, wsum);
@@ -428,91 +622,126 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
 }
 
 // ------------------------------------------------------------------ router, backward
-// One warp per token.  With q the weights' distribution (the softmax over all
+BSQ_DEV void store4(float *p, const float d[4]) { *reinterpret_cast<float4 *>(p) = make_float4(d[0], d[1], d[2], d[3]); }
+BSQ_DEV void store4(uint16_t *p, const float d[4]) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]));
+}
+
+// LPT lanes per token.  With q the weights' distribution (the softmax over all
 // experts, or over the chosen ones) and a_e = dL/dweight of expert e (zero
 // where it was not chosen): dz_e = q_e (a_e - sum q a).  The balance loss adds
 // the softmax's gradient of sum_e b_e p_e with b_e = dloss coef E c_e / (k n^2),
 // kept in shared memory for the CTA.  The chosen experts' own terms reach the
-// lanes that hold those experts through a row of shared memory per warp, which
-// is zero between tokens.
-template <typename In, int EPL, bool NEED_P>
+// lanes that hold those experts through a row of shared memory per token,
+// which is zero between tokens.
+template <typename In, int LPT, int Q, bool NEED_P>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
-                                                        int k, int renorm, const int32_t *__restrict__ ids,
+                                                        int vec, int k, int renorm, const int32_t *__restrict__ ids,
                                                         const float *__restrict__ weights,
                                                         const float *__restrict__ dweights,
                                                         const int32_t *__restrict__ counts, float coef,
                                                         const float *__restrict__ dloss, In *__restrict__ dlogits,
                                                         int64_t ldd) {
-    __shared__ float own_rows[8][EPL * 32];
-    __shared__ float bias[NEED_P ? EPL * 32 : 1];
-    const int lane = threadIdx.x & 31;
-    float *own_row = own_rows[threadIdx.x >> 5];
-#pragma unroll
-    for (int i = 0; i < EPL; i++) own_row[i * 32 + lane] = 0.0f;
+    constexpr int kGroups = 32 / LPT, kCols = 4 * LPT * Q;
+    __shared__ __align__(16) float own_rows[8 * kGroups][kCols];
+    __shared__ __align__(16) float bias[NEED_P ? kCols : 4];
+    const int lane = threadIdx.x & 31, sub = lane % LPT;
+    const int group = threadIdx.x / LPT;
+    float *own_row = own_rows[group];
+    for (int e = sub; e < kCols; e += LPT) own_row[e] = 0.0f;
     if (NEED_P) {
         float bscale = 0.0f;
         if (dloss) {
             const int n = __ldg(counts + E);
             bscale = n > 0 ? __ldg(dloss) * coef * (float)E / (float)n / ((float)k * (float)n) : 0.0f;
         }
-        for (int e = threadIdx.x; e < EPL * 32; e += 256)
+        for (int e = threadIdx.x; e < kCols; e += 256)
             bias[e] = dloss && e < E ? bscale * (float)__ldg(counts + e) : 0.0f;
     }
     __syncthreads();
-    const int64_t stride = (int64_t)gridDim.x * 8;
-    for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += stride) {
-        int e_j = -1;
-        float w_j = 0.0f, a_j = 0.0f;
-        if (lane < k) {
-            e_j = __ldg(ids + t * k + lane);
-            if ((unsigned)e_j >= (unsigned)E) e_j = -1;
-            if (e_j >= 0) {
-                w_j = __ldg(weights + t * k + lane);
-                a_j = dweights ? __ldg(dweights + t * k + lane) : 0.0f;
-            }
+    const int64_t stride = (int64_t)gridDim.x * 8 * kGroups;
+    // a warp's tokens start together: the shuffles want whole warps
+    for (int64_t w0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kGroups; w0 < T; w0 += stride) {
+        const int64_t t = w0 + lane / LPT;
+        const bool in = t < T;
+        float dot = 0.0f;
+        bool live = false;
+        for (int j = sub; j < k; j += LPT) {
+            const int e = in ? __ldg(ids + t * k + j) : -1;
+            if ((unsigned)e >= (unsigned)E) continue;
+            live = true;
+            if (dweights) dot = fmaf(__ldg(weights + t * k + j), __ldg(dweights + t * k + j), dot);
         }
-        float p[EPL];
-        const bool live = __any_sync(kFull, e_j >= 0);  // a masked token's logits are not read
-        if (NEED_P && live) {
-#pragma unroll
-            for (int i = 0; i < EPL; i++) {
-                const int e = i * 32 + lane;
-                p[i] = e < E ? load_logit(logits + t * ldl + e) : -INFINITY;
-            }
-        }
-        const float dot = warp_sum(w_j * a_j);  // sum over chosen of q a: both kinds of q have q_ej = w_j
+        const unsigned any = __ballot_sync(kFull, live);
+        const unsigned mine = LPT == 32 ? kFull : ((1u << (LPT & 31)) - 1u) << (lane & ~(LPT - 1));
+        live = (any & mine) != 0;  // a masked token's logits are not read
+        Row<In, LPT, Q> row;
+        if (NEED_P) row.load(logits + t * ldl, E, sub, vec, live);
+        dot = group_sum<LPT>(dot);  // sum over the chosen of q a: both kinds of q have q_ej = w_j
         // the chosen experts' own term: w_j (a_j - dot), or w_j a_j where dot goes over all experts
-        if (e_j >= 0) own_row[e_j] = renorm ? w_j * (a_j - dot) : w_j * a_j;
-        float d[EPL];
-        if (NEED_P && live) {
-            float top = p[0];
+        if (dweights)
+            for (int j = sub; j < k; j += LPT) {
+                const int e = in ? __ldg(ids + t * k + j) : -1;
+                if ((unsigned)e >= (unsigned)E) continue;
+                own_row[e] = __ldg(weights + t * k + j) * (__ldg(dweights + t * k + j) - (renorm ? dot : 0.0f));
+            }
+        float d[Q][4], sub_all = 0.0f, inv = 0.0f;
+        if (NEED_P) {
+            float top = -INFINITY;
 #pragma unroll
-            for (int i = 1; i < EPL; i++) top = fmaxf(top, p[i]);
-            top = warp_max_redux(top);
-            exp_below<EPL>(p, top);
+            for (int q = 0; q < Q; q++) {
+                row.get(q, d[q]);
+                top = fmaxf(fmaxf(top, fmaxf(d[q][0], d[q][1])), fmaxf(d[q][2], d[q][3]));
+            }
+            top = group_max<LPT>(top);
+            if (!(top > -INFINITY)) top = 0.0f;
+            const f32x2 top2 = f2_pack(top, top);
             float s = 0.0f, pb = 0.0f;
 #pragma unroll
-            for (int i = 0; i < EPL; i++) {
-                d[i] = bias[i * 32 + lane];
-                s += p[i];
-                pb = fmaf(p[i], d[i], pb);
+            for (int q = 0; q < Q; q++) {
+                exp_below4(d[q], top2);
+                const float4 b = *reinterpret_cast<const float4 *>(bias + 4 * (q * LPT + sub));
+                s += (d[q][0] + d[q][1]) + (d[q][2] + d[q][3]);
+                pb += (d[q][0] * b.x + d[q][1] * b.y) + (d[q][2] * b.z + d[q][3] * b.w);
             }
-            const float inv = rcp(warp_sum(s));
-            const float sub = warp_sum(pb) * inv + (renorm ? 0.0f : dot);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < EPL; i++) d[i] = fmaf(p[i] * inv, d[i] - sub, own_row[i * 32 + lane]);
-        } else {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < EPL; i++) d[i] = own_row[i * 32 + lane];
+            s = group_sum<LPT>(s);
+            inv = s > 0.0f ? rcp(s) : 0.0f;
+            sub_all = group_sum<LPT>(pb) * inv + (renorm ? 0.0f : dot);
         }
         __syncwarp();
-        if (e_j >= 0) own_row[e_j] = 0.0f;
-        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < EPL; i++)
-            if (i * 32 + lane < E) store_logit(dlogits + t * ldd + i * 32 + lane, d[i]);
+        for (int q = 0; q < Q; q++) {
+            const int e = 4 * (q * LPT + sub);
+            const float4 o = *reinterpret_cast<const float4 *>(own_row + e);
+            if (NEED_P) {
+                const float4 b = *reinterpret_cast<const float4 *>(bias + e);
+                d[q][0] = fmaf(d[q][0] * inv, b.x - sub_all, o.x);
+                d[q][1] = fmaf(d[q][1] * inv, b.y - sub_all, o.y);
+                d[q][2] = fmaf(d[q][2] * inv, b.z - sub_all, o.z);
+                d[q][3] = fmaf(d[q][3] * inv, b.w - sub_all, o.w);
+            } else {
+                d[q][0] = o.x;
+                d[q][1] = o.y;
+                d[q][2] = o.z;
+                d[q][3] = o.w;
+            }
+            if (!in || e >= E) continue;
+            In *to = dlogits + t * ldd + e;
+            if (vec) {
+                store4(to, d[q]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    if (e + i < E) store_logit(to + i, d[q][i]);
+            }
+        }
+        __syncwarp();
+        if (dweights)
+            for (int j = sub; j < k; j += LPT) {
+                const int e = in ? __ldg(ids + t * k + j) : -1;
+                if ((unsigned)e < (unsigned)E) own_row[e] = 0.0f;
+            }
+        __syncwarp();
     }
 }
 
@@ -762,47 +991,78 @@ int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 int launched() { return cudaGetLastError() == cudaSuccess ? 0 : 1; }
 
+// Whether quads of four logits are aligned in every row.
 template <typename In>
-int route_topk(const RouteArgs &a, const RouteWorkspace &w, int want_p, cudaStream_t s) {
-    const int E = (int)a.E, k = a.topk;
-    // at most 45064 bytes (1024 experts, 32 slots): within the default limit
-    const size_t smem = 8 * (size_t)(E + 1) + 2 * kChunk * (size_t)k + (want_p ? 32 * (size_t)E : 0);
-    auto run = [&](auto kern) {
-        kern<<<(unsigned)w.nchunk, 256, smem, s>>>(
-            static_cast<const In *>(a.logits), a.T, E, a.ldl, a.mask, k, a.renorm, want_p, a.ids, a.weights, a.rows,
-            w.nchunk, reinterpret_cast<uint32_t *>(a.ws + w.hist), reinterpret_cast<float *>(a.ws + w.psum));
-        return launched();
-    };
-    if (E <= 32) return run(route_topk_kernel<In, 1>);
-    if (E <= 64) return run(route_topk_kernel<In, 2>);
-    if (E <= 96) return run(route_topk_kernel<In, 3>);
-    if (E <= 128) return run(route_topk_kernel<In, 4>);
-    if (E <= 192) return run(route_topk_kernel<In, 6>);
-    if (E <= 256) return run(route_topk_kernel<In, 8>);
-    if (E <= 384) return run(route_topk_kernel<In, 12>);
-    if (E <= 512) return run(route_topk_kernel<In, 16>);
-    return run(route_topk_kernel<In, 32>);
+bool quads(const void *p, int64_t E, int64_t ld) {
+    return E % 4 == 0 && ld % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(In)) == 0;
 }
 
-template <typename In, bool NEED_P>
-int route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((a.T + 7) / 8, (int64_t)num_sms * 8);
-    auto run = [&](auto kern) {
-        kern<<<grid, 256, 0, s>>>(static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, a.topk, a.renorm, a.ids,
-                                  a.weights, a.dweights, a.counts, a.coef, a.dloss, static_cast<In *>(a.dlogits),
-                                  a.ldd);
-        return launched();
-    };
-    if (a.E <= 32) return run(route_bwd_kernel<In, 1, NEED_P>);
-    if (a.E <= 64) return run(route_bwd_kernel<In, 2, NEED_P>);
-    if (a.E <= 96) return run(route_bwd_kernel<In, 3, NEED_P>);
-    if (a.E <= 128) return run(route_bwd_kernel<In, 4, NEED_P>);
-    if (a.E <= 192) return run(route_bwd_kernel<In, 6, NEED_P>);
-    if (a.E <= 256) return run(route_bwd_kernel<In, 8, NEED_P>);
-    if (a.E <= 384) return run(route_bwd_kernel<In, 12, NEED_P>);
-    if (a.E <= 512) return run(route_bwd_kernel<In, 16, NEED_P>);
-    return run(route_bwd_kernel<In, 32, NEED_P>);
+// f.template operator()<LPT, Q>() with LPT lanes per token, Q quads of logits per
+// lane.  Eight lanes per token wherever 32 logits per lane are enough: a round
+// of the choice serves four tokens of a warp.
+template <class F>
+int by_experts(int64_t E, F f) {
+    if (E <= 32) return f.template operator()<8, 1>();
+    if (E <= 64) return f.template operator()<8, 2>();
+    if (E <= 96) return f.template operator()<8, 3>();
+    if (E <= 128) return f.template operator()<8, 4>();
+    if (E <= 160) return f.template operator()<8, 5>();
+    if (E <= 192) return f.template operator()<8, 6>();
+    if (E <= 256) return f.template operator()<8, 8>();
+    if (E <= 384) return f.template operator()<16, 6>();
+    if (E <= 512) return f.template operator()<16, 8>();
+    return f.template operator()<32, 8>();
 }
+
+// Shared memory of the first pass; at most 89,608 bytes (1024 experts, 32 slots, 16 warps).
+constexpr int kRouteSmem = 96 * 1024;
+
+template <typename In>
+struct TopkLaunch {
+    const RouteArgs &a;
+    const RouteWorkspace &w;
+    int want_p, num_sms;
+    cudaStream_t s;
+    template <int LPT, int Q>
+    int operator()() const {
+        return w.nchunk == 1 ? run(route_topk_kernel<In, LPT, Q, true>, true)
+                             : run(route_topk_kernel<In, LPT, Q, false>, false);
+    }
+    template <class K>
+    int run(K kern, bool single) const {
+        const int E = (int)a.E, k = a.topk;
+        // 16 warps take the chunk in half as many turns: while all chunks fit on the SMs at once
+        const int threads = w.nchunk <= 2 * num_sms ? 512 : 256;
+        const size_t smem = 8 * (size_t)(E + 1) + 4 * kChunk * (size_t)(k + 1) +
+                            (want_p ? threads / 32 * 4 * (size_t)E : 0) + (single ? 4 * (size_t)(E + 1) : 0) +
+                            2 * kChunk * (size_t)k;
+        if (smem > 48 * 1024 && smem_attr_once(reinterpret_cast<const void *>(kern), kRouteSmem) != BSQ_OK) return 1;
+        const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
+                           a.loss};
+        kern<<<(unsigned)w.nchunk, threads, smem, s>>>(
+            static_cast<const In *>(a.logits), a.T, E, a.ldl, quads<In>(a.logits, E, a.ldl), a.mask,
+            unit_div((uint32_t)k), a.renorm, want_p, out, w.nchunk, reinterpret_cast<uint32_t *>(a.ws + w.hist),
+            reinterpret_cast<float *>(a.ws + w.psum), a.coef);
+        return launched();
+    }
+};
+
+template <typename In, bool NEED_P>
+struct BwdLaunch {
+    const RouteBwdArgs &a;
+    int num_sms;
+    cudaStream_t s;
+    template <int LPT, int Q>
+    int operator()() const {
+        constexpr int per_cta = 8 * (32 / LPT);
+        const unsigned grid = (unsigned)std::min<int64_t>((a.T + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
+        const bool vec = quads<In>(a.logits, a.E, a.ldl) && quads<In>(a.dlogits, a.E, a.ldd);
+        route_bwd_kernel<In, LPT, Q, NEED_P><<<grid, 256, 0, s>>>(
+            static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, vec, a.topk, a.renorm, a.ids, a.weights,
+            a.dweights, a.counts, a.coef, a.dloss, static_cast<In *>(a.dlogits), a.ldd);
+        return launched();
+    }
+};
 
 }  // namespace
 
@@ -820,7 +1080,10 @@ RouteWorkspace route_workspace(int64_t T, int64_t E) {
 int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
     const RouteWorkspace w = route_workspace(a.T, a.E);
     const int want_p = a.prob_sums || a.loss;
-    if (a.bf16 ? route_topk<uint16_t>(a, w, want_p, s) : route_topk<float>(a, w, want_p, s)) return 1;
+    if (a.bf16 ? by_experts(a.E, TopkLaunch<uint16_t>{a, w, want_p, num_sms, s})
+               : by_experts(a.E, TopkLaunch<float>{a, w, want_p, num_sms, s}))
+        return 1;
+    if (w.nchunk == 1) return 0;
     const int E = (int)a.E;
     uint32_t *hist = reinterpret_cast<uint32_t *>(a.ws + w.hist);
     int32_t *first = reinterpret_cast<int32_t *>(a.ws + w.first);
@@ -842,8 +1105,10 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
 int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
     // the softmax over the chosen experts alone needs their weights, not the logits
     if (!a.renorm || a.dloss)
-        return a.bf16 ? route_bwd<uint16_t, true>(a, num_sms, s) : route_bwd<float, true>(a, num_sms, s);
-    return a.bf16 ? route_bwd<uint16_t, false>(a, num_sms, s) : route_bwd<float, false>(a, num_sms, s);
+        return a.bf16 ? by_experts(a.E, BwdLaunch<uint16_t, true>{a, num_sms, s})
+                      : by_experts(a.E, BwdLaunch<float, true>{a, num_sms, s});
+    return a.bf16 ? by_experts(a.E, BwdLaunch<uint16_t, false>{a, num_sms, s})
+                  : by_experts(a.E, BwdLaunch<float, false>{a, num_sms, s});
 }
 
 int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
