@@ -651,7 +651,9 @@ int bsq_moe_combine_bwd(const void *dout, int64_t ldo, const void *y, int64_t ld
     if (y && (y_codes || y_sf)) return BSQ_ERR_INVALID;       // one form of y, not both
     if (!y && (!y_codes != !y_sf)) return BSQ_ERR_INVALID;    // codes and scales come together
     if (y ? ldy < H : H % 32 != 0) return BSQ_ERR_INVALID;
-    if (topk > bsq::kRouteMaxTopk || T >= (int64_t(1) << 31) || H > (int64_t(1) << 25)) return BSQ_ERR_UNSUPPORTED;
+    if (topk > bsq::kRouteMaxTopk || T >= (int64_t(1) << 31) || T * topk >= (int64_t(1) << 31) ||
+        H > (int64_t(1) << 25))
+        return BSQ_ERR_UNSUPPORTED;
     if (T > 0 && (!rows || !weights || !dweights)) return BSQ_ERR_INVALID;
     if (T > 0 && H > 0 && (!dout || (R > 0 && (!dy || (!y && !y_codes))))) return BSQ_ERR_INVALID;
     if (!aligned16(dout) || !aligned16(y) || !aligned16(y_codes) || !aligned16(y_sf) || !aligned16(dy) || ldo % 8 ||

@@ -771,61 +771,87 @@ __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict
                                                                pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
 }
 
-// Eight values of an MXFP8 row: codes times 2^(scale code - 127).
-BSQ_DEV void load8_mx(const uint8_t *codes, const uint8_t *sf, int64_t r, int64_t c, int64_t K, float v[8]) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(codes + r * K + c));
-    const float scale = exp2i((int)__ldg(sf + sf_offset(r, c >> 5, K >> 5)) - 127);
-    e4m3x2_to_f32(q.x & 0xFFFFu, v[0], v[1]);
-    e4m3x2_to_f32(q.x >> 16, v[2], v[3]);
-    e4m3x2_to_f32(q.y & 0xFFFFu, v[4], v[5]);
-    e4m3x2_to_f32(q.y >> 16, v[6], v[7]);
+// 16 values of an MXFP8 row from their codes and the block's scale code.
+BSQ_DEV void mx_decode16(uint4 q, uint32_t sb, f32x2 v[8]) {
+    const float scale = exp2i((int)sb - 127);
+    const f32x2 s2 = f2_pack(scale, scale);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int i = 0; i < 8; i++) v[i] *= scale;
+    for (int i = 0; i < 4; i++) {
+        float a, b, c, d;
+        e4m3x2_to_f32(w[i] & 0xFFFFu, a, b);
+        e4m3x2_to_f32(w[i] >> 16, c, d);
+        v[2 * i] = f2_mul(f2_pack(a, b), s2);
+        v[2 * i + 1] = f2_mul(f2_pack(c, d), s2);
+    }
 }
 
-// dy[rows_tj] = w_tj dout_t and dw_tj = <dout_t, y[rows_tj]>: one CTA per
-// token, row by row; the dot product is summed per warp, then over the warps.
+// Eight columns: the dot product's terms, and w times dout in bf16.
+BSQ_DEV void bwd8(uint4 dq, const float v[8], float w, float &dot, uint4 *to) {
+    const uint32_t d[4] = {dq.x, dq.y, dq.z, dq.w};
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float d0 = bf16_lo(d[i]), d1 = bf16_hi(d[i]);
+        dot = fmaf(d0, v[2 * i], dot);
+        dot = fmaf(d1, v[2 * i + 1], dot);
+        o[i] = pack_bf16(w * d0, w * d1);
+    }
+    *to = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// dy[rows_tj] = w_tj dout_t and dw_tj = <dout_t, y[rows_tj]>: one warp per
+// slot, so that empty slots cost nothing and no sum leaves the warp; a
+// token's dout is read from DRAM by one of its warps and by the others from
+// L1.  Memory bound: y read once, dy written once.
 template <bool MX>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__restrict__ dout, int64_t ldo,
                                                           const uint16_t *__restrict__ y, int64_t ldy,
                                                           const uint8_t *__restrict__ codes,
                                                           const uint8_t *__restrict__ sf, int64_t R, int64_t H,
                                                           const int32_t *__restrict__ rows,
-                                                          const float *__restrict__ weights, int k,
+                                                          const float *__restrict__ weights, uint32_t slots, UnitDiv k,
                                                           uint16_t *__restrict__ dy, int64_t lddy,
                                                           float *__restrict__ dweights) {
-    __shared__ float part[kRouteMaxTopk][8];
-    const int64_t t = blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int j = 0; j < k; j++) {
-        const int64_t r = __ldg(rows + t * k + j);
-        float dot = 0.0f;
-        if (r >= 0 && r < R) {
-            const float w = __ldg(weights + t * k + j);
-            for (int64_t c = threadIdx.x * 8; c < H; c += 256 * 8) {
-                float d[8], v[8];
-                load8_bf16(dout + t * ldo + c, d);
-                if (MX) load8_mx(codes, sf, r, c, H, v);
-                else load8_bf16(y + r * ldy + c, v);
+    const uint32_t slot = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (slot >= slots) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t r = __ldg(rows + slot);
+    float dot = 0.0f;
+    if (r >= 0 && r < R) {
+        const float w = __ldg(weights + slot);
+        const uint16_t *drow = dout + (int64_t)divide(slot, k) * ldo;
+        uint16_t *to = dy + r * lddy;
+        if (MX) {
+            const uint8_t *crow = codes + r * H;
+            const uint8_t *srow = sf + sf_offset(r, 0, H >> 5);
+#pragma unroll 2
+            for (int64_t c = lane * 16; c < H; c += 512) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(crow + c));
+                const uint4 d0 = __ldg(reinterpret_cast<const uint4 *>(drow + c));
+                const uint4 d1 = __ldg(reinterpret_cast<const uint4 *>(drow + c + 8));
+                const uint32_t sb = __ldg(srow + ((c >> 7) << 9) + ((c >> 5) & 3));  // an atom per four blocks
+                f32x2 v2[8];
+                mx_decode16(q, sb, v2);
+                float v[16];
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    dot += d[i] * v[i];
-                    d[i] *= w;
-                }
-                *reinterpret_cast<uint4 *>(dy + r * lddy + c) = make_uint4(
-                    pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+                for (int i = 0; i < 8; i++) f2_unpack(v2[i], v[2 * i], v[2 * i + 1]);
+                bwd8(d0, v, w, dot, reinterpret_cast<uint4 *>(to + c));
+                bwd8(d1, v + 8, w, dot, reinterpret_cast<uint4 *>(to + c + 8));
+            }
+        } else {
+            const uint16_t *yrow = y + r * ldy;
+#pragma unroll 4
+            for (int64_t c = lane * 8; c < H; c += 256) {
+                float v[8];
+                const uint4 d = __ldg(reinterpret_cast<const uint4 *>(drow + c));
+                load8_bf16(yrow + c, v);
+                bwd8(d, v, w, dot, reinterpret_cast<uint4 *>(to + c));
             }
         }
-        dot = warp_sum(dot);
-        if (lane == 0) part[j][warp] = dot;
     }
-    __syncthreads();
-    if (threadIdx.x < k) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; w++) s += part[threadIdx.x][w];
-        dweights[t * k + threadIdx.x] = s;
-    }
+    dot = warp_sum(dot);
+    if (lane == 0) dweights[slot] = dot;
 }
 
 // ------------------------------------------------------------------ gated SiLU with an MXFP8 checkpoint
@@ -922,21 +948,6 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint16_t *__rest
             for (int w = 1; w < 8; w++) top = max(top, part[w]);
             atomicMax(amax, top << 16);  // non-negative floats order as their bits
         }
-    }
-}
-
-// 16 values of an MXFP8 row from their codes and the block's scale code.
-BSQ_DEV void mx_decode16(uint4 q, uint32_t sb, f32x2 v[8]) {
-    const float scale = exp2i((int)sb - 127);
-    const f32x2 s2 = f2_pack(scale, scale);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        float a, b, c, d;
-        e4m3x2_to_f32(w[i] & 0xFFFFu, a, b);
-        e4m3x2_to_f32(w[i] >> 16, c, d);
-        v[2 * i] = f2_mul(f2_pack(a, b), s2);
-        v[2 * i + 1] = f2_mul(f2_pack(c, d), s2);
     }
 }
 
@@ -1121,12 +1132,13 @@ int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, con
 int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y, int64_t ldy, const uint8_t *codes,
                            const uint8_t *sf, int64_t R, int64_t H, const int32_t *rows, const float *weights,
                            int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, int, cudaStream_t s) {
-    if (y)
-        combine_bwd_kernel<false><<<(unsigned)T, 256, 0, s>>>(dout, ldo, y, ldy, codes, sf, R, H, rows, weights, topk,
-                                                              dy, lddy, dweights);
-    else
-        combine_bwd_kernel<true><<<(unsigned)T, 256, 0, s>>>(dout, ldo, y, ldy, codes, sf, R, H, rows, weights, topk,
-                                                             dy, lddy, dweights);
+    const uint32_t slots = (uint32_t)(T * topk);
+    auto run = [&](auto kern) {
+        kern<<<(slots + 7) / 8, 256, 0, s>>>(dout, ldo, y, ldy, codes, sf, R, H, rows, weights, slots,
+                                             unit_div((uint32_t)topk), dy, lddy, dweights);
+    };
+    if (codes) run(combine_bwd_kernel<true>);
+    else run(combine_bwd_kernel<false>);
     return launched();
 }
 

@@ -473,7 +473,8 @@ BSQ_API int bsq_moe_combine(const void *y_bf16, int64_t R, int64_t H, int64_t ld
  * listed by at most one slot (the router's rows are).  y is bf16 (y_bf16,
  * ldy), or the 8-bit form it was kept in (y_bf16 NULL): MXFP8 codes [R][H]
  * and swizzled scales as bsq_quant_mxfp8 writes them, H % 32 == 0.  dy may
- * not overlap the inputs. */
+ * not overlap the inputs.  topk > 32, H > 2^25 or T * topk >= 2^31:
+ * BSQ_ERR_UNSUPPORTED. */
 BSQ_API int bsq_moe_combine_bwd(const void *dout_bf16, int64_t ldo, const void *y_bf16, int64_t ldy,
                                 const uint8_t *y_codes_dev, const uint8_t *y_sf_dev, int64_t R, int64_t H,
                                 const int32_t *rows_dev, const float *weights_dev, int64_t T, int topk,
@@ -488,7 +489,7 @@ BSQ_API int bsq_moe_combine_bwd(const void *dout_bf16, int64_t ldo, const void *
  * n_rows_dev (int32, or NULL for M): only the first min(M, *n_rows_dev) rows
  * exist (for instance row_offsets + E of bsq_moe_route, whose last rows are
  * empty slots); the others are neither read nor written.  F % 32 == 0;
- * ldu >= 2F. */
+ * ldu >= 2F.  M * F >= 2^35 (or M or F >= 2^31): BSQ_ERR_UNSUPPORTED. */
 BSQ_API int bsq_swiglu_ckpt(const void *u_bf16, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows_dev,
                             void *h_bf16_dev, int64_t ldh, uint8_t *codes_dev, uint8_t *sf_dev, float *amax_dev,
                             void *stream);
