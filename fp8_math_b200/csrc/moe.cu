@@ -906,12 +906,11 @@ BSQ_DEV void store16(uint16_t *p, const uint32_t w[8]) {
 // Memory bound: 8.06 bytes per h.  A thread takes 16 columns of the gate and
 // the same 16 of v (64 bytes in flight), so two lanes share a block of 32 and
 // write one scale byte each.
-__global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F,
+__global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F,
                                                           int64_t ldu, UnitDiv per, const int32_t *__restrict__ n_rows,
                                                           uint16_t *__restrict__ h, int64_t ldh,
                                                           uint8_t *__restrict__ codes, uint8_t *__restrict__ sf,
                                                           unsigned int *__restrict__ amax) {
-    __shared__ unsigned int part[8];
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;  // even: a block's two lanes go together
     uint32_t top = 0;
@@ -940,14 +939,9 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_kernel(const uint16_t *__rest
         sf[sf_offset(r, (c + (odd ? F : 0)) >> 5, F >> 4)] = (uint8_t)(odd ? sv : sg);
     }
     if (amax) {
-        top = max(top & 0xFFFFu, top >> 16);
-        top = __reduce_max_sync(kFull, top);
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < 8; w++) top = max(top, part[w]);
-            atomicMax(amax, top << 16);  // non-negative floats order as their bits
-        }
+        top = __reduce_max_sync(kFull, max(top & 0xFFFFu, top >> 16)) << 16;
+        // non-negative floats order as their bits; most warps find a larger one there already
+        if ((threadIdx.x & 31) == 0 && top > *reinterpret_cast<volatile unsigned int *>(amax)) atomicMax(amax, top);
     }
 }
 
@@ -1144,7 +1138,7 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
 
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
                        int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 16) + 255) / 256, (int64_t)num_sms * 8);
+    const unsigned grid = (unsigned)(M * (F / 16) + 255) / 256;
     swiglu_ckpt_kernel<<<grid, 256, 0, s>>>(u, M, F, ldu, unit_div((uint32_t)(F / 16)), n_rows, h, ldh, codes, sf,
                                             amax);
     return launched();
@@ -1153,7 +1147,7 @@ int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, con
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
                            int64_t F, const int32_t *n_rows, uint16_t *du, int64_t lddu, uint16_t *h, int64_t ldh,
                            int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)std::min<int64_t>((M * (F / 16) + 255) / 256, (int64_t)num_sms * 8);
+    const unsigned grid = (unsigned)(M * (F / 16) + 255) / 256;
     const UnitDiv per = unit_div((uint32_t)(F / 16));
     if (h) swiglu_ckpt_bwd_kernel<true><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);
     else swiglu_ckpt_bwd_kernel<false><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);
