@@ -35,20 +35,15 @@ BSQ_DEV float load_logit(const uint16_t *p) { return __uint_as_float((uint32_t)_
 BSQ_DEV void store_logit(float *p, float v) { *p = v; }
 BSQ_DEV void store_logit(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
 
-// 2^x (relative error 2^-22, subnormal results kept) and 1/x (1 ulp).
+// 2^x (relative error 2^-22, results below 2^-126 are 0) and 1/x of a normal x (1 ulp).
 BSQ_DEV float ex2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 BSQ_DEV float rcp(float x) {
     float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-BSQ_DEV float ex2_ftz(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 constexpr float kLog2e = 1.44269504088896341f;
@@ -156,8 +151,8 @@ BSQ_DEV void exp_below4(float x[4], f32x2 top2) {
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
         f2_unpack(f2_mul(f2_sub(f2_pack(x[i], x[i + 1]), top2), l2), x[i], x[i + 1]);
-        x[i] = ex2_ftz(x[i]);
-        x[i + 1] = ex2_ftz(x[i + 1]);
+        x[i] = ex2(x[i]);
+        x[i + 1] = ex2(x[i + 1]);
     }
 }
 
@@ -359,7 +354,7 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
                 const float z = c.pop(row, sub, e);
                 const bool ok = z > -INFINITY;
                 if (j == 0 && ok) top = z;
-                const float x = ok ? ex2_ftz((z - top) * kLog2e) : 0.0f;
+                const float x = ok ? ex2((z - top) * kLog2e) : 0.0f;
                 chosen += x;
                 if (ok && sub == j - j0) {
                     my_e = e;
@@ -856,20 +851,24 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__rest
 
 // ------------------------------------------------------------------ gated SiLU with an MXFP8 checkpoint
 // sigmoid(g) as r or e r with e = exp(-|g|), r = 1 / (1 + e): e never
-// overflows and r lies in [1/2, 1].  Relative error (8 + |g|) 2^-24 at most,
-// the |g| from the rounding of the exponent; results are rounded to 2^-8.
+// overflows and r lies in [1/2, 1].  e is the square of 2^(-|g| log2(e) / 2),
+// so that its subnormal values come from an ordinary product.  Relative error
+// (13 + 2 |g|) 2^-24 at most, the |g| from the rounding of the exponent;
+// results are rounded to 2^-8.
 BSQ_DEV float sigmoid(float g) {
-    const float e = ex2(-fabsf(g) * kLog2e);
+    const float half = ex2(fabsf(g) * (-0.5f * kLog2e));
+    const float e = half * half;
     const float r = rcp(1.0f + e);
-    return g >= 0.0f ? r : e * r;
+    return (g >= 0.0f ? 1.0f : e) * r;
 }
 
-// max(|a|, |b|) of two bf16 pairs
-BSQ_DEV uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
+// Larger of two bf16 pairs of magnitudes, lane by lane.
+BSQ_DEV uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
-    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+constexpr uint32_t kAbs2 = 0x7FFF7FFFu;
 
 // Row-wise MXFP8 of 16 values, two lanes per block of 32 (the bytes of
 // bsq_quant_mxfp8 with nearest rounding).  The block maximum is taken on the
@@ -877,9 +876,10 @@ BSQ_DEV uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
 // would be below 0, and for an all-zero block, whose codes are +0), and the
 // products with 2^-E are exact.
 BSQ_DEV uint4 mx_encode16(const uint32_t w[8], uint32_t *scale_code) {
-    uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(w[0], w[1]), absmax_bf16x2(w[2], w[3])),
-                               absmax_bf16x2(absmax_bf16x2(w[4], w[5]), absmax_bf16x2(w[6], w[7])));
-    m = absmax_bf16x2(m, __shfl_xor_sync(kFull, m, 1));
+    uint32_t m = w[0] & kAbs2;
+#pragma unroll
+    for (int i = 1; i < 8; i++) m = max_bf16x2(m, w[i] & kAbs2);
+    m = max_bf16x2(m, __shfl_xor_sync(kFull, m, 1));
     m = max(m & 0xFFFFu, m >> 16);
     const uint32_t sb = (uint32_t)max((int)(m >> 7) - 8, 0);
     *scale_code = sb;
@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__r
         for (int q = 0; q < 8; q++) {
             const float g0 = bf16_lo(g[q]), g1 = bf16_hi(g[q]);
             o[q] = pack_bf16(g0 * sigmoid(g0) * bf16_lo(v[q]), g1 * sigmoid(g1) * bf16_hi(v[q]));
-            top = absmax_bf16x2(top, o[q]);
+            top = max_bf16x2(top, o[q] & kAbs2);
         }
         store16(h + r * ldh + c, o);
         uint8_t *row = codes + (int64_t)r * 2 * F + c;

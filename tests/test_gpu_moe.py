@@ -9,7 +9,8 @@ chain of operations, and one rounding of the output type (bf16: 2^-8).  An
 exponential e^d of d = x - max is formed as 2^(d log2 e): the roundings of the
 difference, of the product and of the constant are each |d| U in d, so 3 |d| U
 in e^d; ex2.approx adds 4 U (2^-22), rcp.approx 2 U, a product or sum 1 U per
-step.  In the sigmoid d = -|g| is exact, which leaves 2 |g| U."""
+step.  In the sigmoid d = -|g| is exact, which leaves 2 |g| U, and e^d is the
+square of 2^(d log2 e / 2): 2 x 4 U and the product."""
 import numpy as np
 import pytest
 import torch
@@ -291,15 +292,15 @@ def gate_input(M, F, seed):
 
 
 def swiglu_tol(u, want):
-    """The sigmoid (2 |g| + 4 for the exponential, 1 + e, the reciprocal 2, e r) and two products, all U; bf16's
+    """The sigmoid (2 |g| + 9 for the exponential, 1 + e, the reciprocal 2, e r) and two products, all U; bf16's
     rounding, whose subnormal half step is 2^-134."""
-    return (B + (2 * np.minimum(abs(u[:, :u.shape[1] // 2]), 104) + 10) * U) * abs(want) + 1e-40
+    return (B + (2 * np.minimum(abs(u[:, :u.shape[1] // 2]), 104) + 15) * U) * abs(want) + 1e-40
 
 
 def swiglu_bwd_tol(u, mag, want):
     """The same sigmoid, 1 - s (its error is that of s), and five products and sums, relative to mag."""
     g = np.minimum(abs(u[:, :u.shape[1] // 2]), 104)
-    t = (2 * (2 * np.concatenate([g, g], 1) + 8) + 6) * U * mag
+    t = (2 * (2 * np.concatenate([g, g], 1) + 13) + 6) * U * mag
     return t + B * (abs(want) + t) + 1e-40
 
 
