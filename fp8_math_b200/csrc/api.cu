@@ -686,8 +686,8 @@ int bsq_swiglu_ckpt(const void *u, int64_t M, int64_t F, int64_t ldu, const int3
     DeviceState *d;
     if (int st = device_state(&d)) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (amax && cudaMemsetAsync(amax, 0, sizeof(float), s) != cudaSuccess) return BSQ_ERR_CUDA;
-    if (M == 0 || F == 0) return BSQ_OK;
+    if (M == 0 || F == 0)
+        return !amax || cudaMemsetAsync(amax, 0, sizeof(float), s) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
     return bsq::launch_swiglu_ckpt(static_cast<const uint16_t *>(u), M, F, ldu, n_rows, static_cast<uint16_t *>(h),
                                    ldh, codes, sf, reinterpret_cast<unsigned int *>(amax), d->num_sms, s)
                ? BSQ_ERR_CUDA

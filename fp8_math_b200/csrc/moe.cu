@@ -903,6 +903,11 @@ BSQ_DEV void store16(uint16_t *p, const uint32_t w[8]) {
     reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+__global__ void zero_word_kernel(unsigned int *p) {
+    grid_dependents_launch();
+    *p = 0;
+}
+
 // Memory bound: 8.06 bytes per h.  A thread takes 16 columns of the gate and
 // the same 16 of v (64 bytes in flight), so two lanes share a block of 32 and
 // write one scale byte each.
@@ -939,6 +944,9 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__r
         sf[sf_offset(r, (c + (odd ? F : 0)) >> 5, F >> 4)] = (uint8_t)(odd ? sv : sg);
     }
     if (amax) {
+        // zero_word_kernel, the launch before this one, has started after all earlier work was done: only
+        // the word that it zeroes has to wait for it
+        grid_dependency_wait();
         top = __reduce_max_sync(kFull, max(top & 0xFFFFu, top >> 16)) << 16;
         // non-negative floats order as their bits; most warps find a larger one there already
         if ((threadIdx.x & 31) == 0 && top > *reinterpret_cast<volatile unsigned int *>(amax)) atomicMax(amax, top);
@@ -1137,17 +1145,22 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
 }
 
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
-                       int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)(M * (F / 16) + 255) / 256;
-    swiglu_ckpt_kernel<<<grid, 256, 0, s>>>(u, M, F, ldu, unit_div((uint32_t)(F / 16)), n_rows, h, ldh, codes, sf,
-                                            amax);
-    return launched();
+                       int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int, cudaStream_t s) {
+    const unsigned grid = (unsigned)((M * (F / 16) + 255) / 256);
+    const UnitDiv per = unit_div((uint32_t)(F / 16));
+    if (!amax) {
+        swiglu_ckpt_kernel<<<grid, 256, 0, s>>>(u, M, F, ldu, per, n_rows, h, ldh, codes, sf, amax);
+        return launched();
+    }
+    zero_word_kernel<<<1, 1, 0, s>>>(amax);
+    return launched() || launch_dependent(swiglu_ckpt_kernel, dim3(grid), dim3(256), 0, s, u, M, F, ldu, per, n_rows, h,
+                                          ldh, codes, sf, amax) != cudaSuccess;
 }
 
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
                            int64_t F, const int32_t *n_rows, uint16_t *du, int64_t lddu, uint16_t *h, int64_t ldh,
                            int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)(M * (F / 16) + 255) / 256;
+    const unsigned grid = (unsigned)((M * (F / 16) + 255) / 256);
     const UnitDiv per = unit_div((uint32_t)(F / 16));
     if (h) swiglu_ckpt_bwd_kernel<true><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);
     else swiglu_ckpt_bwd_kernel<false><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);

@@ -56,7 +56,7 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
                            int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, int num_sms,
                            cudaStream_t s);
 
-// amax (may be NULL) is zeroed by the caller.
+// amax may be NULL.
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
                        int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int num_sms, cudaStream_t s);
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
