@@ -270,6 +270,130 @@ struct Candidates<float, LPT, Q> {
     }
 };
 
+// For k <= L: a sorted list of the token's L best, built without a branch: a
+// lane sorts its logits by networks of maxima and minima, and log2(LPT)
+// exchanges merge the lanes' lists (the larger of a[i] and b[L-1-i] are the L
+// best of two sorted lists, in bitonic order).  Against rounds of one maximum
+// each this took 131072x256, k = 8, from 77 to 48 us and 16384x64 from 9.0 to
+// 6.4 us.  The entries are logits with the expert in their low bits, as above.
+// An fp32 logit gives its lowest ceil(log2 E) bits for it; where two such
+// truncated logits meet in the list or at its end, the order is not certain and
+// the warp's tokens go through the rounds instead.  NaN entries (-inf logits)
+// sink to the end.
+BSQ_DEV void order2(float &a, float &b) {
+    const float lo = min_nan(a, b);
+    a = fmaxf(a, b);
+    b = lo;
+}
+// Batcher's odd-even merge sort, descending, for N = 4 or 8.
+template <int N>
+BSQ_DEV void sort_desc(float *v) {
+#pragma unroll
+    for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+        for (int k = p; k; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; i++)
+                    if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order2(v[i + j], v[i + j + k]);
+}
+// v becomes the N best of the sorted lists v and w, sorted.
+template <int N>
+BSQ_DEV void keep_best(float *v, const float *w) {
+#pragma unroll
+    for (int i = 0; i < N; i++) v[i] = fmaxf(v[i], w[N - 1 - i]);
+#pragma unroll
+    for (int h = N / 2; h; h >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; i++)
+            if (!(i & h)) order2(v[i], v[i + h]);
+}
+template <int N>
+BSQ_DEV float entry(const float *v, int i) {
+    float r = v[0];
+#pragma unroll
+    for (int j = 1; j < N; j++) r = i == j ? v[j] : r;
+    return r;
+}
+template <typename In>
+BSQ_DEV uint32_t expert_bits(int E) {
+    return sizeof(In) == 2 ? 0xFFFFu : (2u << (31 - __clz(max(E - 1, 1)))) - 1u;
+}
+BSQ_DEV float with_expert(float z, uint32_t e, uint32_t bits) {
+    const uint32_t b = __float_as_uint(__fadd_rn(z, 0.0f));
+    return __uint_as_float((b & ~bits) | (e ^ (~(uint32_t)((int32_t)b >> 31) & bits)));
+}
+BSQ_DEV int expert_of(uint32_t b, uint32_t bits) { return (int)((b ^ ~(uint32_t)((int32_t)b >> 31)) & bits); }
+
+// The token's L best, the same list in all of its lanes.
+template <int L, typename In, int LPT, int Q>
+BSQ_DEV void best_list(const Row<In, LPT, Q> &row, int sub, uint32_t bits, float v[L]) {
+    constexpr int kQuads = L / 4;  // quads that make a list
+#pragma unroll
+    for (int q0 = 0; q0 < Q; q0 += kQuads) {
+        float w[L];
+#pragma unroll
+        for (int d = 0; d < kQuads; d++) {
+            const int q = q0 + d;
+            float z[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (q < Q) row.get(q, z);
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                w[4 * d + i] = q < Q ? with_expert(z[i], (uint32_t)(4 * (q * LPT + sub) + i), bits) : -INFINITY;
+        }
+        sort_desc<L>(w);
+        if (q0 == 0) {
+#pragma unroll
+            for (int i = 0; i < L; i++) v[i] = w[i];
+        } else {
+            keep_best<L>(v, w);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < LPT; o <<= 1) {
+        float w[L];
+#pragma unroll
+        for (int i = 0; i < L; i++) w[i] = __shfl_xor_sync(kFull, v[i], o);
+        keep_best<L>(v, w);
+    }
+}
+
+// Slot `sub` of the token by such a list: its expert (-1: none) and logit.
+// False where the order is not certain.
+template <int L, typename In, int LPT, int Q>
+BSQ_DEV bool choose(const Row<In, LPT, Q> &row, const In *logits, int sub, int E, int k, int &e, float &z) {
+    const uint32_t bits = expert_bits<In>(E);
+    float v[L];
+    best_list<L>(row, sub, bits, v);
+    const float mine = entry<L>(v, sub);
+    const uint32_t b = __float_as_uint(mine);
+    e = sub < k && mine > -INFINITY ? expert_of(b, bits) : -1;
+    if (sizeof(In) == 2) {
+        z = __uint_as_float(b & ~bits);
+        return true;
+    }
+    z = e >= 0 ? load_logit(logits + e) : 0.0f;
+    const uint32_t next = __shfl_down_sync(kFull, b, 1, LPT);
+    bool bad = sub + 1 < k && e >= 0 && ((b ^ next) & ~bits) == 0;
+    // the last slot's truncated logit: nothing else may have it
+    const float last = entry<L>(v, k - 1);
+    const uint32_t lb = __float_as_uint(last);
+    const float floor = __uint_as_float((lb >> 31) ? lb | bits : lb & ~bits);
+    int n = 0;
+#pragma unroll
+    for (int q = 0; q < Q; q++) {
+        float x[4];
+        row.get(q, x);
+#pragma unroll
+        for (int i = 0; i < 4; i++) n += x[i] >= floor;
+    }
+#pragma unroll
+    for (int o = LPT / 2; o; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
+    bad |= last > -INFINITY && n != k;
+    return !__any_sync(kFull, bad);
+}
+
 // Exclusive scan of n[0..E) (PAD128: each rounded up to 128) into off[0..E]
 // by the CTA's first warp, 32 consecutive experts at a time.
 template <bool PAD128, class Count>
@@ -297,6 +421,9 @@ BSQ_DEV float balance_loss(float weighted, int tokens, float coef, int E, int k)
     return tokens > 0 ? coef * (float)E * (weighted / (float)tokens) / ((float)k * (float)tokens) : 0.0f;
 }
 
+// Bytes of one chunk's row of 8-bit counts (E experts and the tokens).
+__host__ __device__ __forceinline__ int hist_row(int E) { return (E + 1 + 3) & ~3; }
+
 struct RouteOut {
     int32_t *ids;
     float *weights;
@@ -309,13 +436,15 @@ struct RouteOut {
 // go into one 64-bit mask of tokens per expert, whose population count is the
 // chunk's count and whose bits below a token are that token's rank in the
 // chunk: the order "by expert, then token" needs no sort.  Row E of the counts
-// is the number of tokens with at least one expert.  SINGLE: the chunk is all
-// there is, and the CTA finishes the call (offsets, rows, loss).
-template <typename In, int LPT, int Q, bool SINGLE>
+// is the number of tokens with at least one expert.  Where the chunk is all
+// there is, the CTA finishes the call (offsets, rows, loss).  L: k <= L by
+// sorted lists; 0: rounds for any k.
+template <typename In, int LPT, int Q, int L>
 __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                          int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
                                                          int renorm, int want_p, RouteOut out, int64_t nchunk,
-                                                         uint32_t *__restrict__ hist, float *__restrict__ psum,
+                                                         uint32_t *__restrict__ hist, uint8_t *__restrict__ hist8,
+                                                         float *__restrict__ psum, unsigned int *__restrict__ ticket,
                                                          float coef) {
     grid_dependents_launch();
     extern __shared__ unsigned long long smem[];
@@ -324,14 +453,21 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
     float *sel_x = reinterpret_cast<float *>(words + 2 * (E + 1));     // [kChunk][k] exp(logit - top)
     float *inv = sel_x + kChunk * k;                                   // [kChunk]
     float *red = inv + kChunk;                                         // [nwarps][E] when want_p
-    int32_t *off = reinterpret_cast<int32_t *>(red + (want_p ? nwarps * E : 0));  // [E + 1] when SINGLE
-    uint16_t *sel = reinterpret_cast<uint16_t *>(off + (SINGLE ? E + 1 : 0));     // [kChunk][k]
+    int32_t *off = reinterpret_cast<int32_t *>(red + (want_p ? nwarps * E : 0));  // [E + 1] when nchunk == 1
+    uint16_t *sel = reinterpret_cast<uint16_t *>(off + (nchunk == 1 ? E + 1 : 0));     // [kChunk][k]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPT;
     constexpr int kGroups = 32 / LPT;
     for (int i = threadIdx.x; i < 2 * (E + 1); i += blockDim.x) words[i] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * kChunk;
     const int here = (int)min((int64_t)kChunk, T - t0);
+    const bool single = nchunk == 1;
+    auto pick = [&](int tl, int j, int e, float x) {
+        sel[tl * k + j] = (uint16_t)e;
+        sel_x[tl * k + j] = x;
+        if (e >= 0) atomicOr(&words[2 * e + (tl >> 5)], 1u << (tl & 31));
+        if (j == 0 && e >= 0) atomicOr(&words[2 * E + (tl >> 5)], 1u << (tl & 31));
+    };
     float acc[Q][4];
 #pragma unroll
     for (int q = 0; q < Q; q++)
@@ -343,33 +479,38 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
         const bool live = in && (!mask || __ldg(mask + t0 + tl) != 0);
         Row<In, LPT, Q> row;
         row.load(logits + (t0 + tl) * ldl, E, sub, vec, live);
-        Candidates<In, LPT, Q> c;
-        c.template fill<false>(row, sub, 0.0f);
         float top = 0.0f, chosen = 0.0f;
-        for (int j0 = 0; j0 < k; j0 += LPT) {
-            int my_e = -1;
-            float my_x = 0.0f;
-            for (int j = j0; j < min(k, j0 + LPT); j++) {
-                int e;
-                const float z = c.pop(row, sub, e);
-                const bool ok = z > -INFINITY;
-                if (j == 0 && ok) top = z;
-                const float x = ok ? ex2((z - top) * kLog2e) : 0.0f;
-                chosen += x;
-                if (ok && sub == j - j0) {
-                    my_e = e;
-                    my_x = x;
-                }
+        bool done = false;
+        if (L > 0) {
+            int e;
+            float z;
+            done = choose<L == 0 ? 4 : L>(row, logits + (t0 + tl) * ldl, sub, E, k, e, z);
+            if (done) {  // the same for the whole warp
+                top = __shfl_sync(kFull, e >= 0 ? z : 0.0f, lane & ~(LPT - 1));
+                const float x = e >= 0 ? ex2((z - top) * kLog2e) : 0.0f;
+                chosen = group_sum<LPT>(x);
+                if (in && sub < k) pick(tl, sub, e, x);
             }
-            // a lane per slot
-            const int j = j0 + sub;
-            if (in && j < k) {
-                sel[tl * k + j] = (uint16_t)my_e;
-                sel_x[tl * k + j] = my_x;
-                if (my_e >= 0) {
-                    atomicOr(&words[2 * my_e + (tl >> 5)], 1u << (tl & 31));
-                    if (j == 0) atomicOr(&words[2 * E + (tl >> 5)], 1u << (tl & 31));
+        }
+        if (!done) {
+            Candidates<In, LPT, Q> c;
+            c.template fill<false>(row, sub, 0.0f);
+            for (int j0 = 0; j0 < k; j0 += LPT) {
+                int my_e = -1;
+                float my_x = 0.0f;
+                for (int j = j0; j < min(k, j0 + LPT); j++) {
+                    int e;
+                    const float z = c.pop(row, sub, e);
+                    const bool ok = z > -INFINITY;
+                    if (j == 0 && ok) top = z;
+                    const float x = ok ? ex2((z - top) * kLog2e) : 0.0f;
+                    chosen += x;
+                    if (ok && sub == j - j0) {
+                        my_e = e;
+                        my_x = x;
+                    }
                 }
+                if (in && j0 + sub < k) pick(tl, j0 + sub, my_e, my_x);  // a lane per slot
             }
         }
         if (want_p || !renorm) {
@@ -406,7 +547,7 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
             }
     }
     __syncthreads();
-    if (SINGLE) {
+    if (single) {
         if (warp == 0) warp_scan<false>([&](int e) { return __popcll(smem[e]); }, E, off);
         __syncthreads();
     }
@@ -414,7 +555,7 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
         const int tl = (int)divide((uint32_t)i, kd);
         const int e = (int16_t)sel[i];
         int row = e < 0 ? -1 : __popcll(smem[e] & ((1ull << tl) - 1ull));
-        if (SINGLE && e >= 0) {
+        if (single && e >= 0) {
             row += off[e];
             out.row_index[row] = tl;
         }
@@ -422,12 +563,18 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
         out.weights[t0 * k + i] = sel_x[i] * inv[tl];
         out.rows[t0 * k + i] = row;
     }
-    if (!SINGLE) {
+    if (!single) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
         for (int e = threadIdx.x; e <= E; e += blockDim.x) {
             const unsigned long long m = smem[e];
-            // count in the low byte, the chunk's first token of the expert above it
-            hist[(int64_t)e * nchunk + blockIdx.x] =
-                (uint32_t)__popcll(m) | (m ? (uint32_t)(__ffsll(m) - 1) << 8 : 0u);
+            const uint32_t n = (uint32_t)__popcll(m), first = m ? (uint32_t)(__ffsll(m) - 1) : 0u;
+            if (hist8) {  // a row of counts and a row of first tokens per chunk
+                uint8_t *to = hist8 + (int64_t)blockIdx.x * 2 * hist_row(E);
+                to[e] = (uint8_t)n;
+                to[hist_row(E) + e] = (uint8_t)first;
+            } else {  // a row per expert: count in the low byte, first token above it
+                hist[(int64_t)e * nchunk + blockIdx.x] = n | first << 8;
+            }
             if (want_p && e < E) {
                 float v = 0.0f;
                 for (int w = 0; w < nwarps; w++) v += red[w * E + e];
@@ -613,6 +760,122 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
         }
         scan_counts<true>(counts, E, off, wsum);
         for (int e = threadIdx.x; e <= E; e += 256) sf_row_off[e] = off[e];
+    }
+}
+
+// Passes 2 and 3 in one launch, for few chunks: a CTA per chunk adds up all
+// chunks' 8-bit counts (kSmallHist bytes at most, from L2), those before its own
+// apart, which gives the experts' offsets and its own prefix, and places its
+// slots.  Two counts share a 32-bit sum: 64 a chunk, 512 chunks at most.  The
+// experts' sums of probabilities are spread over the CTAs; the last CTA to
+// finish makes the loss of them, in a fixed order.
+constexpr int kSmallHist = 48 * 1024, kSmallChunks = 512;
+
+__global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDiv kd, int E, int nchunk,
+                                                               const uint8_t *__restrict__ hist8,
+                                                               const float *__restrict__ psum, RouteOut out,
+                                                               float *psum_total, unsigned int *ticket, float coef) {
+    grid_dependents_launch();
+    grid_dependency_wait();
+    __shared__ int32_t tot[kRouteMaxExperts + 4], base[kRouteMaxExperts + 4], off[kRouteMaxExperts + 1];
+    __shared__ int first_chunk;
+    __shared__ unsigned int turn;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = (int)kd.d;
+    const int row = hist_row(E), words = row / 4, chunk = blockIdx.x;
+    const uint32_t slot0 = (uint32_t)chunk * kChunk * k;
+    const int here = (int)min((int64_t)kChunk, T - (int64_t)chunk * kChunk) * k;
+    // this chunk's slots, read ahead of the sums
+    int e_s[2], rank_s[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int j = threadIdx.x + 256 * i;
+        e_s[i] = j < here ? out.ids[slot0 + j] : -1;
+        rank_s[i] = j < here ? out.rows[slot0 + j] : 0;
+    }
+    for (int e = threadIdx.x; e < row; e += 256) tot[e] = base[e] = 0;
+    if (threadIdx.x == 0) first_chunk = nchunk;
+    __syncthreads();
+    {
+        const int parts = max(1, 256 / words);  // threads that share a word, each with every parts-th chunk
+        for (int u = threadIdx.x; u < words * parts; u += 256) {
+            const int w = u % words, part = u / words;
+            uint32_t t0 = 0, t1 = 0, b0 = 0, b1 = 0;
+#pragma unroll 8
+            for (int c = part; c < nchunk; c += parts) {
+                const uint32_t x = __ldg(reinterpret_cast<const uint32_t *>(hist8 + (int64_t)c * 2 * row) + w);
+                const uint32_t x0 = x & 0x00FF00FFu, x1 = (x >> 8) & 0x00FF00FFu;
+                t0 += x0;
+                t1 += x1;
+                if (c < chunk) {
+                    b0 += x0;
+                    b1 += x1;
+                }
+            }
+            atomicAdd(&tot[4 * w], (int)(t0 & 0xFFFFu));
+            atomicAdd(&tot[4 * w + 1], (int)(t1 & 0xFFFFu));
+            atomicAdd(&tot[4 * w + 2], (int)(t0 >> 16));
+            atomicAdd(&tot[4 * w + 3], (int)(t1 >> 16));
+            atomicAdd(&base[4 * w], (int)(b0 & 0xFFFFu));
+            atomicAdd(&base[4 * w + 1], (int)(b1 & 0xFFFFu));
+            atomicAdd(&base[4 * w + 2], (int)(b0 >> 16));
+            atomicAdd(&base[4 * w + 3], (int)(b1 >> 16));
+        }
+    }
+    __syncthreads();
+    if (warp == 0) warp_scan<false>([&](int e) { return tot[e]; }, E, off);
+    __syncthreads();
+    const int total = off[E];
+    for (int j = threadIdx.x, i = 0; j < here; j += 256, i++) {
+        const int e = i < 2 ? e_s[i] : out.ids[slot0 + j];
+        if (e < 0) continue;
+        const int r = off[e] + base[e] + (i < 2 ? rank_s[i] : out.rows[slot0 + j]);
+        out.rows[slot0 + j] = r;
+        out.row_index[r] = chunk * kChunk + (int)divide((uint32_t)j, kd);
+    }
+    if ((int64_t)slot0 + here > total) {  // rows without a slot repeat the first row's token
+        int token = 0;
+        if (total > 0) {
+            int e0 = 0;
+            while (off[e0 + 1] == 0) e0++;
+            for (int c = threadIdx.x; c < nchunk; c += 256)
+                if (hist8[(int64_t)c * 2 * row + e0]) {
+                    atomicMin(&first_chunk, c);
+                    break;
+                }
+            __syncthreads();
+            token = first_chunk * kChunk + hist8[(int64_t)first_chunk * 2 * row + row + e0];
+        }
+        for (int j = threadIdx.x; j < here; j += 256)
+            if ((int)slot0 + j >= total) out.row_index[slot0 + j] = token;
+    }
+    if (chunk == 0) {
+        for (int e = threadIdx.x; e <= E; e += 256) {
+            out.counts[e] = tot[e];
+            out.row_off[e] = off[e];
+        }
+        if (warp == 1) warp_scan<true>([&](int e) { return tot[e]; }, E, out.sf_row_off);
+    }
+    if (!psum) return;
+    for (int e = chunk + nchunk * warp; e < E; e += nchunk * 8) {  // one warp per expert
+        float p = 0.0f;
+        for (int c = lane; c < nchunk; c += 32) p += __ldg(psum + (int64_t)e * nchunk + c);
+        p = warp_sum(p);
+        if (lane == 0) {
+            psum_total[e] = p;
+            if (out.prob_sums) out.prob_sums[e] = p;
+            __threadfence();
+        }
+    }
+    if (!out.loss) return;
+    __syncthreads();
+    if (threadIdx.x == 0) turn = atomicAdd(ticket, 1u);
+    __syncthreads();
+    if (turn == gridDim.x - 1 && warp == 0) {
+        __threadfence();
+        float v = 0.0f;
+        for (int e = lane; e < E; e += 32) v += (float)tot[e] * __ldcg(psum_total + e);
+        v = warp_sum(v);
+        if (lane == 0) *out.loss = balance_loss(v, tot[E], coef, E, k);
     }
 }
 
@@ -1027,6 +1290,8 @@ int by_experts(int64_t E, F f) {
     return f.template operator()<32, 8>();
 }
 
+bool small_hist(int64_t nchunk, int E) { return nchunk <= kSmallChunks && nchunk * hist_row(E) <= kSmallHist; }
+
 // Shared memory of the first pass; at most 89,608 bytes (1024 experts, 32 slots, 16 warps).
 constexpr int kRouteSmem = 96 * 1024;
 
@@ -1038,16 +1303,17 @@ struct TopkLaunch {
     cudaStream_t s;
     template <int LPT, int Q>
     int operator()() const {
-        return w.nchunk == 1 ? run(route_topk_kernel<In, LPT, Q, true>, true)
-                             : run(route_topk_kernel<In, LPT, Q, false>, false);
+        return a.topk <= 4   ? run(route_topk_kernel<In, LPT, Q, 4>)
+               : a.topk <= 8 ? run(route_topk_kernel<In, LPT, Q, 8>)
+                             : run(route_topk_kernel<In, LPT, Q, 0>);
     }
     template <class K>
-    int run(K kern, bool single) const {
+    int run(K kern) const {
         const int E = (int)a.E, k = a.topk;
         // 16 warps take the chunk in half as many turns: while all chunks fit on the SMs at once
         const int threads = w.nchunk <= 2 * num_sms ? 512 : 256;
         const size_t smem = 8 * (size_t)(E + 1) + 4 * kChunk * (size_t)(k + 1) +
-                            (want_p ? threads / 32 * 4 * (size_t)E : 0) + (single ? 4 * (size_t)(E + 1) : 0) +
+                            (want_p ? threads / 32 * 4 * (size_t)E : 0) + (w.nchunk == 1 ? 4 * (size_t)(E + 1) : 0) +
                             2 * kChunk * (size_t)k;
         if (smem > 48 * 1024 && smem_attr_once(reinterpret_cast<const void *>(kern), kRouteSmem) != BSQ_OK) return 1;
         const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
@@ -1055,7 +1321,8 @@ struct TopkLaunch {
         kern<<<(unsigned)w.nchunk, threads, smem, s>>>(
             static_cast<const In *>(a.logits), a.T, E, a.ldl, quads<In>(a.logits, E, a.ldl), a.mask,
             unit_div((uint32_t)k), a.renorm, want_p, out, w.nchunk, reinterpret_cast<uint32_t *>(a.ws + w.hist),
-            reinterpret_cast<float *>(a.ws + w.psum), a.coef);
+            small_hist(w.nchunk, E) ? a.ws + w.hist : nullptr, reinterpret_cast<float *>(a.ws + w.psum),
+            reinterpret_cast<unsigned int *>(a.ws + w.ticket), a.coef);
         return launched();
     }
 };
@@ -1086,7 +1353,8 @@ RouteWorkspace route_workspace(int64_t T, int64_t E) {
     w.psum = up(w.hist + 4 * (E + 1) * w.nchunk, 256);
     w.first = up(w.psum + 4 * E * w.nchunk, 256);
     w.psum_total = up(w.first + 4 * E, 256);
-    w.bytes = up(w.psum_total + 4 * E, 256);
+    w.ticket = up(w.psum_total + 4 * E, 256);
+    w.bytes = w.ticket + 256;
     return w;
 }
 
@@ -1102,11 +1370,19 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
     int32_t *first = reinterpret_cast<int32_t *>(a.ws + w.first);
     float *psum = want_p ? reinterpret_cast<float *>(a.ws + w.psum) : nullptr;
     float *total = want_p ? reinterpret_cast<float *>(a.ws + w.psum_total) : nullptr;
+    if (small_hist(w.nchunk, E)) {
+        const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
+                           a.loss};
+        return launch_dependent(route_scan_place_kernel, dim3((unsigned)w.nchunk), dim3(256), 0, s, a.T,
+                                unit_div((uint32_t)a.topk), E, (int)w.nchunk, (const uint8_t *)(a.ws + w.hist),
+                                (const float *)psum, out, total, reinterpret_cast<unsigned int *>(a.ws + w.ticket),
+                                a.coef) != cudaSuccess;
+    }
     if (launch_dependent(route_scan_kernel, dim3(E + 1), dim3(256), 0, s, hist, (const float *)psum, w.nchunk, E,
                          a.counts, first, total) != cudaSuccess)
         return 1;
     const int64_t n = a.T * a.topk;
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 1023) / 1024, (int64_t)num_sms * 8));
+    const unsigned grid = (unsigned)std::min<int64_t>((n + 511) / 512, (int64_t)num_sms * 8);
     if (launch_dependent(route_place_kernel, dim3(grid), dim3(256), 0, s, (const int32_t *)a.ids, a.rows, (uint32_t)n,
                          unit_div((uint32_t)a.topk), E, w.nchunk, (const uint32_t *)hist, (const int32_t *)a.counts, (const int32_t *)first,
                          (const float *)total, a.coef, a.row_index, a.row_off, a.sf_row_off, a.prob_sums,

@@ -44,6 +44,10 @@ def logits_of(T, E, seed, bf16=False, kind="normal"):
         low = torch.finfo(torch.bfloat16 if bf16 else torch.float32).min
         z[torch.rand(T, E, generator=g) < 0.7] = low
         z[::4] = low
+    elif kind == "near":        # fp32 values that differ in their last bits only
+        z = 1.0 + torch.randint(0, 300, (T, E), generator=g).float() * 2.0 ** -23
+        z[1::2] *= -1.0
+        z[::3, ::2] = torch.randn(z[::3, ::2].shape, generator=g)
     elif kind == "wide":        # far apart: small probabilities underflow
         z *= 60
     return z.to(torch.bfloat16) if bf16 else z
@@ -78,9 +82,12 @@ def test_route(T, E, k, bf16, renorm):
     check_route(api.moe_route(z, k, renorm=renorm), z, k, None, renorm, None)
 
 
-@pytest.mark.parametrize("kind", ["ties", "shut", "lowest", "wide"])
+@pytest.mark.parametrize("kind", ["ties", "shut", "lowest", "near", "wide"])
 @pytest.mark.parametrize("bf16,renorm,T,E,k", [(False, True, 150, 40, 6), (True, False, 300, 130, 8),
-                                               (True, True, 64, 256, 4), (False, False, 67, 3, 3)])
+                                               (True, True, 64, 256, 4), (False, False, 67, 3, 3),
+                                               (False, True, 70, 512, 8), (False, True, 90, 64, 12),
+                                               (True, True, 33, 700, 16), (False, True, 65, 1000, 2),
+                                               (False, False, 40, 160, 8), (False, True, 30, 256, 1)])
 def test_route_difficult_logits(kind, bf16, renorm, T, E, k):
     z = dev(logits_of(T, E, T + k, bf16, kind))
     mask = dev((torch.rand(T, generator=torch.Generator().manual_seed(4)) < 0.8).to(torch.uint8))
