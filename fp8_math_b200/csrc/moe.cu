@@ -444,9 +444,9 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
                                                          int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
                                                          int renorm, int want_p, RouteOut out, int64_t nchunk,
                                                          uint32_t *__restrict__ hist, uint8_t *__restrict__ hist8,
-                                                         float *__restrict__ psum, unsigned int *__restrict__ ticket,
-                                                         float coef) {
+                                                         float *__restrict__ psum, int64_t stride, float coef) {
     grid_dependents_launch();
+    grid_dependency_wait();
     extern __shared__ unsigned long long smem[];
     const int k = (int)kd.d, nwarps = blockDim.x >> 5;
     unsigned int *words = reinterpret_cast<unsigned int *>(smem);      // [(E + 1) * 2]
@@ -564,7 +564,6 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
         out.rows[t0 * k + i] = row;
     }
     if (!single) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
         for (int e = threadIdx.x; e <= E; e += blockDim.x) {
             const unsigned long long m = smem[e];
             const uint32_t n = (uint32_t)__popcll(m), first = m ? (uint32_t)(__ffsll(m) - 1) : 0u;
@@ -573,12 +572,12 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
                 to[e] = (uint8_t)n;
                 to[hist_row(E) + e] = (uint8_t)first;
             } else {  // a row per expert: count in the low byte, first token above it
-                hist[(int64_t)e * nchunk + blockIdx.x] = n | first << 8;
+                hist[(int64_t)e * stride + blockIdx.x] = n | first << 8;
             }
             if (want_p && e < E) {
                 float v = 0.0f;
                 for (int w = 0; w < nwarps; w++) v += red[w * E + e];
-                psum[(int64_t)e * nchunk + blockIdx.x] = v;
+                psum[hist8 ? (int64_t)blockIdx.x * E + e : (int64_t)e * stride + blockIdx.x] = v;
             }
         }
     } else {
@@ -617,33 +616,55 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
 // Pass 2.  One CTA per expert (and one for the token count): its counts per
 // chunk become exclusive prefixes in place, their total goes to counts[e];
 // the first token that chose e, and the sum of its probabilities, go along.
+// A thread takes eight neighbouring chunks (rows are padded to eight).
 __global__ void __launch_bounds__(256) route_scan_kernel(uint32_t *__restrict__ hist, const float *__restrict__ psum,
-                                                         int64_t nchunk, int E, int32_t *__restrict__ counts,
-                                                         int32_t *__restrict__ first, float *__restrict__ psum_total) {
+                                                         int64_t nchunk, int64_t stride, int E,
+                                                         int32_t *__restrict__ counts, int32_t *__restrict__ first,
+                                                         float *__restrict__ psum_total) {
     grid_dependents_launch();
     grid_dependency_wait();
     __shared__ int wsum[8];
     __shared__ float fsum[8];
     __shared__ int sfirst;
     const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t *h = hist + (int64_t)e * nchunk;
+    uint32_t *h = hist + (int64_t)e * stride;
     if (threadIdx.x == 0) sfirst = 0x7FFFFFFF;
     __syncthreads();
     int carry = 0;
     float p = 0.0f;
-    for (int64_t c0 = 0; c0 < nchunk; c0 += 256) {
-        const int64_t c = c0 + threadIdx.x;
-        const uint32_t v = c < nchunk ? h[c] : 0u;
-        const int n = (int)(v & 0xFFu);
-        if (n) atomicMin(&sfirst, (int)(c * kChunk) + (int)(v >> 8));
-        if (psum && e < E && c < nchunk) p += psum[(int64_t)e * nchunk + c];
-        int s = n;
+    for (int64_t c0 = 0; c0 < nchunk; c0 += 2048) {
+        const int64_t c = c0 + threadIdx.x * 8;
+        uint32_t v[8] = {};
+        if (c < nchunk) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(h + c), b = *reinterpret_cast<const uint4 *>(h + c + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            if (psum && e < E) {
+                const float *q = psum + (int64_t)e * stride + c;
+                const float4 x = __ldg(reinterpret_cast<const float4 *>(q)), y = __ldg(reinterpret_cast<const float4 *>(q + 4));
+                const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    if (c + i < nchunk) p += f[i];
+            }
+        }
+        int s = 0, low = 0x7FFFFFFF;
+#pragma unroll
+        for (int i = 7; i >= 0; i--) {
+            if (c + i >= nchunk) v[i] = 0;  // the padding was never written
+            if (v[i] & 0xFFu) low = (int)((c + i) * kChunk) + (int)(v[i] >> 8);
+            v[i] &= 0xFFu;
+            s += (int)v[i];
+        }
+        low = __reduce_min_sync(kFull, low);
+        if (lane == 0 && low != 0x7FFFFFFF) atomicMin(&sfirst, low);
+        int inc = s;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, s, o);
-            if (lane >= o) s += u;
+            const int u = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += u;
         }
-        if (lane == 31) wsum[warp] = s;
+        if (lane == 31) wsum[warp] = inc;
         __syncthreads();
         int before = 0, all = 0;
 #pragma unroll
@@ -651,7 +672,17 @@ __global__ void __launch_bounds__(256) route_scan_kernel(uint32_t *__restrict__ 
             if (w < warp) before += wsum[w];
             all += wsum[w];
         }
-        if (c < nchunk) h[c] = (uint32_t)(carry + before + s - n);
+        if (c < nchunk) {
+            uint32_t at = (uint32_t)(carry + before + inc - s);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint32_t n = v[i];
+                v[i] = at;
+                at += n;
+            }
+            *reinterpret_cast<uint4 *>(h + c) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4 *>(h + c + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
         carry += all;
         __syncthreads();
     }
@@ -708,7 +739,7 @@ BSQ_DEV void scan_counts(const int32_t *counts, int E, int32_t *off, int *wsum) 
 // rank inside the chunk; the rows past the last routed one repeat the first
 // row's token.  CTA 0 also writes the offsets and the loss.
 __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ rows,
-                                                          uint32_t n, UnitDiv k, int E, int64_t nchunk,
+                                                          uint32_t n, UnitDiv k, int E, int64_t stride,
                                                           const uint32_t *__restrict__ hist,
                                                           const int32_t *__restrict__ counts,
                                                           const int32_t *__restrict__ first,
@@ -727,15 +758,28 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
         if (off[e] == 0 && off[e + 1] > 0) first_token = first[e];  // one expert only
     __syncthreads();
     const uint32_t total = (uint32_t)off[E];
-    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {  // n < 2^31
-        const int e = ids[i];
-        const uint32_t t = divide(i, k);
-        if (e >= 0) {
-            const int row = off[e] + (int)hist[(int64_t)e * nchunk + t / kChunk] + rows[i];
-            rows[i] = row;
-            row_index[row] = (int32_t)t;
+    // four slots at a time, so that their loads overlap (n < 2^31)
+    for (uint32_t i0 = blockIdx.x * 1024 + threadIdx.x; i0 < n; i0 += gridDim.x * 1024) {
+        int e[4], r[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const uint32_t i = i0 + 256 * u;
+            e[u] = i < n ? __ldg(ids + i) : -1;
+            r[u] = i < n ? rows[i] : 0;
         }
-        if (i >= total) row_index[i] = first_token;
+#pragma unroll
+        for (int u = 0; u < 4; u++)
+            if (e[u] >= 0)
+                r[u] += off[e[u]] + (int)__ldg(hist + (int64_t)e[u] * stride + divide(i0 + 256 * u, k) / kChunk);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const uint32_t i = i0 + 256 * u;
+            if (e[u] >= 0) {
+                rows[i] = r[u];
+                row_index[r[u]] = (int32_t)divide(i, k);
+            }
+            if (i < n && i >= total) row_index[i] = first_token;
+        }
     }
     if (blockIdx.x == 0) {
         for (int e = threadIdx.x; e <= E; e += 256) row_off[e] = off[e];
@@ -766,24 +810,25 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
 // Passes 2 and 3 in one launch, for few chunks: a CTA per chunk adds up all
 // chunks' 8-bit counts (kSmallHist bytes at most, from L2), those before its own
 // apart, which gives the experts' offsets and its own prefix, and places its
-// slots.  Two counts share a 32-bit sum: 64 a chunk, 512 chunks at most.  The
-// experts' sums of probabilities are spread over the CTAs; the last CTA to
-// finish makes the loss of them, in a fixed order.
+// slots.  Three bytes are added before they are widened (64 a chunk), and two
+// counts share a 32-bit sum (512 chunks at most).  One more CTA writes the
+// offsets, the sums of the probabilities and the loss.
 constexpr int kSmallHist = 48 * 1024, kSmallChunks = 512;
 
 __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDiv kd, int E, int nchunk,
-                                                               const uint8_t *__restrict__ hist8,
+                                                               UnitDiv wd, const uint8_t *__restrict__ hist8,
                                                                const float *__restrict__ psum, RouteOut out,
-                                                               float *psum_total, unsigned int *ticket, float coef) {
+                                                               float coef) {
     grid_dependents_launch();
     grid_dependency_wait();
-    __shared__ int32_t tot[kRouteMaxExperts + 4], base[kRouteMaxExperts + 4], off[kRouteMaxExperts + 1];
+    // counts of the chunks before this one, and of this one and the ones after it
+    __shared__ int32_t before[kRouteMaxExperts + 4], rest[kRouteMaxExperts + 4], off[kRouteMaxExperts + 1];
+    __shared__ float sums[kRouteMaxExperts];
     __shared__ int first_chunk;
-    __shared__ unsigned int turn;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = (int)kd.d;
-    const int row = hist_row(E), words = row / 4, chunk = blockIdx.x;
+    const int row = hist_row(E), words = (int)wd.d, chunk = blockIdx.x;
     const uint32_t slot0 = (uint32_t)chunk * kChunk * k;
-    const int here = (int)min((int64_t)kChunk, T - (int64_t)chunk * kChunk) * k;
+    const int here = (int)max((int64_t)0, min((int64_t)kChunk, T - (int64_t)chunk * kChunk)) * k;
     // this chunk's slots, read ahead of the sums
     int e_s[2], rank_s[2];
 #pragma unroll
@@ -792,90 +837,99 @@ __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDi
         e_s[i] = j < here ? out.ids[slot0 + j] : -1;
         rank_s[i] = j < here ? out.rows[slot0 + j] : 0;
     }
-    for (int e = threadIdx.x; e < row; e += 256) tot[e] = base[e] = 0;
+    for (int e = threadIdx.x; e < row; e += 256) before[e] = rest[e] = 0;
     if (threadIdx.x == 0) first_chunk = nchunk;
-    __syncthreads();
-    {
-        const int parts = max(1, 256 / words);  // threads that share a word, each with every parts-th chunk
-        for (int u = threadIdx.x; u < words * parts; u += 256) {
-            const int w = u % words, part = u / words;
-            uint32_t t0 = 0, t1 = 0, b0 = 0, b1 = 0;
-#pragma unroll 8
-            for (int c = part; c < nchunk; c += parts) {
-                const uint32_t x = __ldg(reinterpret_cast<const uint32_t *>(hist8 + (int64_t)c * 2 * row) + w);
-                const uint32_t x0 = x & 0x00FF00FFu, x1 = (x >> 8) & 0x00FF00FFu;
-                t0 += x0;
-                t1 += x1;
-                if (c < chunk) {
-                    b0 += x0;
-                    b1 += x1;
+    if (chunk == nchunk && psum) {
+        // 16 rows of partial sums in flight per thread; E <= 256 here: 256 / E threads share an expert
+        __shared__ float part[256];
+        const int parts = 256 / E, e = threadIdx.x % E, g = threadIdx.x / E;
+        float p = 0.0f;
+        if (g < parts)
+            for (int c0 = g; c0 < nchunk; c0 += 16 * parts) {
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int c = c0 + i * parts;
+                    v[i] = c < nchunk ? __ldg(psum + c * E + e) : 0.0f;
                 }
+#pragma unroll
+                for (int i = 0; i < 16; i++) p += v[i];
             }
-            atomicAdd(&tot[4 * w], (int)(t0 & 0xFFFFu));
-            atomicAdd(&tot[4 * w + 1], (int)(t1 & 0xFFFFu));
-            atomicAdd(&tot[4 * w + 2], (int)(t0 >> 16));
-            atomicAdd(&tot[4 * w + 3], (int)(t1 >> 16));
-            atomicAdd(&base[4 * w], (int)(b0 & 0xFFFFu));
-            atomicAdd(&base[4 * w + 1], (int)(b1 & 0xFFFFu));
-            atomicAdd(&base[4 * w + 2], (int)(b0 >> 16));
-            atomicAdd(&base[4 * w + 3], (int)(b1 >> 16));
+        part[threadIdx.x] = p;
+        __syncthreads();
+        if (threadIdx.x < E) {
+            for (int i = 1; i < parts; i++) p += part[threadIdx.x + i * E];
+            sums[threadIdx.x] = p;
+            if (out.prob_sums) out.prob_sums[threadIdx.x] = p;
         }
     }
     __syncthreads();
-    if (warp == 0) warp_scan<false>([&](int e) { return tot[e]; }, E, off);
+    const int parts = max(1, 256 / words);  // threads that share a word, each with every parts-th chunk
+    for (int u = threadIdx.x; u < words * parts; u += 256) {
+        const int part = (int)divide((uint32_t)u, wd), w = u - part * words;
+        auto add_up = [&](int c0, int c1, int32_t *to) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(hist8) + w;
+            uint32_t even = 0, odd = 0;
+            int c = c0 + part;
+#pragma unroll 2
+            for (; c + 2 * parts < c1; c += 3 * parts) {
+                const uint32_t x = __ldg(p + c * 2 * words) + __ldg(p + (c + parts) * 2 * words) +
+                                   __ldg(p + (c + 2 * parts) * 2 * words);
+                even += x & 0x00FF00FFu;
+                odd += (x >> 8) & 0x00FF00FFu;
+            }
+            for (; c < c1; c += parts) {
+                const uint32_t x = __ldg(p + c * 2 * words);
+                even += x & 0x00FF00FFu;
+                odd += (x >> 8) & 0x00FF00FFu;
+            }
+            if (even & 0xFFFFu) atomicAdd(to + 4 * w, (int)(even & 0xFFFFu));
+            if (odd & 0xFFFFu) atomicAdd(to + 4 * w + 1, (int)(odd & 0xFFFFu));
+            if (even >> 16) atomicAdd(to + 4 * w + 2, (int)(even >> 16));
+            if (odd >> 16) atomicAdd(to + 4 * w + 3, (int)(odd >> 16));
+        };
+        add_up(0, chunk, before);
+        add_up(chunk, nchunk, rest);
+    }
+    __syncthreads();
+    if (warp == 0) warp_scan<false>([&](int e) { return before[e] + rest[e]; }, E, off);
     __syncthreads();
     const int total = off[E];
     for (int j = threadIdx.x, i = 0; j < here; j += 256, i++) {
         const int e = i < 2 ? e_s[i] : out.ids[slot0 + j];
         if (e < 0) continue;
-        const int r = off[e] + base[e] + (i < 2 ? rank_s[i] : out.rows[slot0 + j]);
+        const int r = off[e] + before[e] + (i < 2 ? rank_s[i] : out.rows[slot0 + j]);
         out.rows[slot0 + j] = r;
         out.row_index[r] = chunk * kChunk + (int)divide((uint32_t)j, kd);
     }
-    if ((int64_t)slot0 + here > total) {  // rows without a slot repeat the first row's token
+    if (here > 0 && (int64_t)slot0 + here > total) {  // rows without a slot repeat the first row's token
         int token = 0;
         if (total > 0) {
             int e0 = 0;
             while (off[e0 + 1] == 0) e0++;
             for (int c = threadIdx.x; c < nchunk; c += 256)
-                if (hist8[(int64_t)c * 2 * row + e0]) {
+                if (hist8[c * 2 * row + e0]) {
                     atomicMin(&first_chunk, c);
                     break;
                 }
             __syncthreads();
-            token = first_chunk * kChunk + hist8[(int64_t)first_chunk * 2 * row + row + e0];
+            token = first_chunk * kChunk + hist8[first_chunk * 2 * row + row + e0];
         }
         for (int j = threadIdx.x; j < here; j += 256)
             if ((int)slot0 + j >= total) out.row_index[slot0 + j] = token;
     }
-    if (chunk == 0) {
-        for (int e = threadIdx.x; e <= E; e += 256) {
-            out.counts[e] = tot[e];
-            out.row_off[e] = off[e];
-        }
-        if (warp == 1) warp_scan<true>([&](int e) { return tot[e]; }, E, out.sf_row_off);
+    if (chunk < nchunk) return;
+    // the CTA past the chunks: `before` holds the counts
+    for (int e = threadIdx.x; e <= E; e += 256) {
+        out.counts[e] = before[e];
+        out.row_off[e] = off[e];
     }
-    if (!psum) return;
-    for (int e = chunk + nchunk * warp; e < E; e += nchunk * 8) {  // one warp per expert
-        float p = 0.0f;
-        for (int c = lane; c < nchunk; c += 32) p += __ldg(psum + (int64_t)e * nchunk + c);
-        p = warp_sum(p);
-        if (lane == 0) {
-            psum_total[e] = p;
-            if (out.prob_sums) out.prob_sums[e] = p;
-            __threadfence();
-        }
-    }
-    if (!out.loss) return;
-    __syncthreads();
-    if (threadIdx.x == 0) turn = atomicAdd(ticket, 1u);
-    __syncthreads();
-    if (turn == gridDim.x - 1 && warp == 0) {
-        __threadfence();
+    if (warp == 0) warp_scan<true>([&](int e) { return before[e]; }, E, out.sf_row_off);
+    if (warp == 1 && out.loss) {
         float v = 0.0f;
-        for (int e = lane; e < E; e += 32) v += (float)tot[e] * __ldcg(psum_total + e);
+        for (int e = lane; e < E; e += 32) v += (float)before[e] * sums[e];
         v = warp_sum(v);
-        if (lane == 0) *out.loss = balance_loss(v, tot[E], coef, E, k);
+        if (lane == 0) *out.loss = balance_loss(v, before[E], coef, E, k);
     }
 }
 
@@ -900,6 +954,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ l
                                                         const int32_t *__restrict__ counts, float coef,
                                                         const float *__restrict__ dloss, In *__restrict__ dlogits,
                                                         int64_t ldd) {
+    grid_dependents_launch();
+    grid_dependency_wait();
     constexpr int kGroups = 32 / LPT, kCols = 4 * LPT * Q;
     __shared__ __align__(16) float own_rows[8 * kGroups][kCols];
     __shared__ __align__(16) float bias[NEED_P ? kCols : 4];
@@ -1010,6 +1066,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict
                                                       const int32_t *__restrict__ rows,
                                                       const float *__restrict__ weights, int k,
                                                       uint16_t *__restrict__ out, int64_t ldo) {
+    grid_dependents_launch();
+    grid_dependency_wait();
     const int64_t t = blockIdx.x;
     const int64_t c = ((int64_t)blockIdx.y * 128 + threadIdx.x) * 8;
     if (c >= H) return;
@@ -1071,6 +1129,8 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__rest
                                                           const float *__restrict__ weights, uint32_t slots, UnitDiv k,
                                                           uint16_t *__restrict__ dy, int64_t lddy,
                                                           float *__restrict__ dweights) {
+    grid_dependents_launch();
+    grid_dependency_wait();
     const uint32_t slot = blockIdx.x * 8 + (threadIdx.x >> 5);
     if (slot >= slots) return;
     const int lane = threadIdx.x & 31;
@@ -1167,7 +1227,8 @@ BSQ_DEV void store16(uint16_t *p, const uint32_t w[8]) {
 }
 
 __global__ void zero_word_kernel(unsigned int *p) {
-    grid_dependents_launch();
+    grid_dependency_wait();
+    grid_dependents_launch();  // not before: the next kernel relies on all earlier work being done
     *p = 0;
 }
 
@@ -1179,6 +1240,10 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__r
                                                           uint16_t *__restrict__ h, int64_t ldh,
                                                           uint8_t *__restrict__ codes, uint8_t *__restrict__ sf,
                                                           unsigned int *__restrict__ amax) {
+    grid_dependents_launch();
+    // with amax, zero_word_kernel before this one has waited for all earlier work; only the word that it
+    // zeroes has to wait for it, at the end
+    if (!amax) grid_dependency_wait();
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;  // even: a block's two lanes go together
     uint32_t top = 0;
@@ -1207,8 +1272,6 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__r
         sf[sf_offset(r, (c + (odd ? F : 0)) >> 5, F >> 4)] = (uint8_t)(odd ? sv : sg);
     }
     if (amax) {
-        // zero_word_kernel, the launch before this one, has started after all earlier work was done: only
-        // the word that it zeroes has to wait for it
         grid_dependency_wait();
         top = __reduce_max_sync(kFull, max(top & 0xFFFFu, top >> 16)) << 16;
         // non-negative floats order as their bits; most warps find a larger one there already
@@ -1226,6 +1289,8 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__
                                                               UnitDiv per, const int32_t *__restrict__ n_rows,
                                                               uint16_t *__restrict__ du, int64_t lddu,
                                                               uint16_t *__restrict__ h, int64_t ldh) {
+    grid_dependents_launch();
+    grid_dependency_wait();
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
@@ -1290,7 +1355,9 @@ int by_experts(int64_t E, F f) {
     return f.template operator()<32, 8>();
 }
 
-bool small_hist(int64_t nchunk, int E) { return nchunk <= kSmallChunks && nchunk * hist_row(E) <= kSmallHist; }
+bool small_hist(int64_t nchunk, int E) {
+    return E <= 256 && nchunk <= kSmallChunks && nchunk * hist_row(E) <= kSmallHist;
+}
 
 // Shared memory of the first pass; at most 89,608 bytes (1024 experts, 32 slots, 16 warps).
 constexpr int kRouteSmem = 96 * 1024;
@@ -1318,12 +1385,12 @@ struct TopkLaunch {
         if (smem > 48 * 1024 && smem_attr_once(reinterpret_cast<const void *>(kern), kRouteSmem) != BSQ_OK) return 1;
         const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
                            a.loss};
-        kern<<<(unsigned)w.nchunk, threads, smem, s>>>(
-            static_cast<const In *>(a.logits), a.T, E, a.ldl, quads<In>(a.logits, E, a.ldl), a.mask,
-            unit_div((uint32_t)k), a.renorm, want_p, out, w.nchunk, reinterpret_cast<uint32_t *>(a.ws + w.hist),
-            small_hist(w.nchunk, E) ? a.ws + w.hist : nullptr, reinterpret_cast<float *>(a.ws + w.psum),
-            reinterpret_cast<unsigned int *>(a.ws + w.ticket), a.coef);
-        return launched();
+        return launch_dependent(
+                   kern, dim3((unsigned)w.nchunk), dim3(threads), smem, s, static_cast<const In *>(a.logits), a.T, E,
+                   a.ldl, (int)quads<In>(a.logits, E, a.ldl), a.mask, unit_div((uint32_t)k), (int)a.renorm, want_p, out,
+                   w.nchunk, reinterpret_cast<uint32_t *>(a.ws + w.hist),
+                   small_hist(w.nchunk, E) ? a.ws + w.hist : (uint8_t *)nullptr,
+                   reinterpret_cast<float *>(a.ws + w.psum), w.stride, a.coef) != cudaSuccess;
     }
 };
 
@@ -1337,10 +1404,10 @@ struct BwdLaunch {
         constexpr int per_cta = 8 * (32 / LPT);
         const unsigned grid = (unsigned)std::min<int64_t>((a.T + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
         const bool vec = quads<In>(a.logits, a.E, a.ldl) && quads<In>(a.dlogits, a.E, a.ldd);
-        route_bwd_kernel<In, LPT, Q, NEED_P><<<grid, 256, 0, s>>>(
-            static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, vec, a.topk, a.renorm, a.ids, a.weights,
-            a.dweights, a.counts, a.coef, a.dloss, static_cast<In *>(a.dlogits), a.ldd);
-        return launched();
+        return launch_dependent(route_bwd_kernel<In, LPT, Q, NEED_P>, dim3(grid), dim3(256), 0, s,
+                                static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, (int)vec, a.topk,
+                                (int)a.renorm, a.ids, a.weights, a.dweights, a.counts, a.coef, a.dloss,
+                                static_cast<In *>(a.dlogits), a.ldd) != cudaSuccess;
     }
 };
 
@@ -1349,12 +1416,12 @@ struct BwdLaunch {
 RouteWorkspace route_workspace(int64_t T, int64_t E) {
     RouteWorkspace w;
     w.nchunk = std::max<int64_t>((T + kChunk - 1) / kChunk, 1);
+    w.stride = up(w.nchunk, 8);
     w.hist = 0;
-    w.psum = up(w.hist + 4 * (E + 1) * w.nchunk, 256);
-    w.first = up(w.psum + 4 * E * w.nchunk, 256);
+    w.psum = up(w.hist + 4 * (E + 1) * w.stride, 256);
+    w.first = up(w.psum + 4 * E * w.stride, 256);
     w.psum_total = up(w.first + 4 * E, 256);
-    w.ticket = up(w.psum_total + 4 * E, 256);
-    w.bytes = w.ticket + 256;
+    w.bytes = up(w.psum_total + 4 * E, 256);
     return w;
 }
 
@@ -1373,18 +1440,17 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
     if (small_hist(w.nchunk, E)) {
         const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
                            a.loss};
-        return launch_dependent(route_scan_place_kernel, dim3((unsigned)w.nchunk), dim3(256), 0, s, a.T,
-                                unit_div((uint32_t)a.topk), E, (int)w.nchunk, (const uint8_t *)(a.ws + w.hist),
-                                (const float *)psum, out, total, reinterpret_cast<unsigned int *>(a.ws + w.ticket),
-                                a.coef) != cudaSuccess;
+        return launch_dependent(route_scan_place_kernel, dim3((unsigned)w.nchunk + 1), dim3(256), 0, s, a.T,
+                                unit_div((uint32_t)a.topk), E, (int)w.nchunk,
+                                unit_div((uint32_t)hist_row(E) / 4), (const uint8_t *)(a.ws + w.hist), (const float *)psum, out, a.coef) != cudaSuccess;
     }
-    if (launch_dependent(route_scan_kernel, dim3(E + 1), dim3(256), 0, s, hist, (const float *)psum, w.nchunk, E,
-                         a.counts, first, total) != cudaSuccess)
+    if (launch_dependent(route_scan_kernel, dim3(E + 1), dim3(256), 0, s, hist, (const float *)psum, w.nchunk,
+                         w.stride, E, a.counts, first, total) != cudaSuccess)
         return 1;
     const int64_t n = a.T * a.topk;
-    const unsigned grid = (unsigned)std::min<int64_t>((n + 511) / 512, (int64_t)num_sms * 8);
+    const unsigned grid = (unsigned)std::min<int64_t>((n + 1023) / 1024, (int64_t)num_sms * 8);
     if (launch_dependent(route_place_kernel, dim3(grid), dim3(256), 0, s, (const int32_t *)a.ids, a.rows, (uint32_t)n,
-                         unit_div((uint32_t)a.topk), E, w.nchunk, (const uint32_t *)hist, (const int32_t *)a.counts, (const int32_t *)first,
+                         unit_div((uint32_t)a.topk), E, w.stride, (const uint32_t *)hist, (const int32_t *)a.counts, (const int32_t *)first,
                          (const float *)total, a.coef, a.row_index, a.row_off, a.sf_row_off, a.prob_sums,
                          a.loss) != cudaSuccess)
         return 1;
@@ -1402,9 +1468,8 @@ int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
 
 int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
                        int64_t T, int topk, uint16_t *out, int64_t ldo, int, cudaStream_t s) {
-    combine_kernel<<<dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), 128, 0, s>>>(y, R, H, ldy, rows, weights, topk,
-                                                                                     out, ldo);
-    return launched();
+    return launch_dependent(combine_kernel, dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), dim3(128), 0, s, y, R, H,
+                            ldy, rows, weights, topk, out, ldo) != cudaSuccess;
 }
 
 int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y, int64_t ldy, const uint8_t *codes,
@@ -1412,25 +1477,19 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
                            int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, int, cudaStream_t s) {
     const uint32_t slots = (uint32_t)(T * topk);
     auto run = [&](auto kern) {
-        kern<<<(slots + 7) / 8, 256, 0, s>>>(dout, ldo, y, ldy, codes, sf, R, H, rows, weights, slots,
-                                             unit_div((uint32_t)topk), dy, lddy, dweights);
+        return launch_dependent(kern, dim3((slots + 7) / 8), dim3(256), 0, s, dout, ldo, y, ldy, codes, sf, R, H, rows,
+                                weights, slots, unit_div((uint32_t)topk), dy, lddy, dweights) != cudaSuccess;
     };
-    if (codes) run(combine_bwd_kernel<true>);
-    else run(combine_bwd_kernel<false>);
-    return launched();
+    return codes ? run(combine_bwd_kernel<true>) : run(combine_bwd_kernel<false>);
 }
 
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
                        int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int, cudaStream_t s) {
     const unsigned grid = (unsigned)((M * (F / 16) + 255) / 256);
     const UnitDiv per = unit_div((uint32_t)(F / 16));
-    if (!amax) {
-        swiglu_ckpt_kernel<<<grid, 256, 0, s>>>(u, M, F, ldu, per, n_rows, h, ldh, codes, sf, amax);
-        return launched();
-    }
-    zero_word_kernel<<<1, 1, 0, s>>>(amax);
-    return launched() || launch_dependent(swiglu_ckpt_kernel, dim3(grid), dim3(256), 0, s, u, M, F, ldu, per, n_rows, h,
-                                          ldh, codes, sf, amax) != cudaSuccess;
+    if (amax && launch_dependent(zero_word_kernel, dim3(1), dim3(1), 0, s, amax) != cudaSuccess) return 1;
+    return launch_dependent(swiglu_ckpt_kernel, dim3(grid), dim3(256), 0, s, u, M, F, ldu, per, n_rows, h, ldh, codes,
+                            sf, amax) != cudaSuccess;
 }
 
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
@@ -1438,9 +1497,11 @@ int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *code
                            int num_sms, cudaStream_t s) {
     const unsigned grid = (unsigned)((M * (F / 16) + 255) / 256);
     const UnitDiv per = unit_div((uint32_t)(F / 16));
-    if (h) swiglu_ckpt_bwd_kernel<true><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);
-    else swiglu_ckpt_bwd_kernel<false><<<grid, 256, 0, s>>>(dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h, ldh);
-    return launched();
+    auto run = [&](auto kern) {
+        return launch_dependent(kern, dim3(grid), dim3(256), 0, s, dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h,
+                                ldh) != cudaSuccess;
+    };
+    return h ? run(swiglu_ckpt_bwd_kernel<true>) : run(swiglu_ckpt_bwd_kernel<false>);
 }
 
 }  // namespace bsq
