@@ -230,28 +230,26 @@ def quant_nvfp4_gather(x, row_index, four_over_six=False, rht_mask=None, groups=
 
 
 # ---------------------------------------------------------------- mixture-of-experts training step
-def _need(fn, ok):
-    """The library sees pointers only: shapes, types and devices are checked here."""
-    if not ok:
-        raise bsq.BsqError(fn, bsq.BSQ_ERR_INVALID)
+# The library sees pointers only: types, shapes and devices are checked here,
+# with as few calls per tensor as will do (a rollout's calls take microseconds).
+def _refuse(fn):
+    raise bsq.BsqError(fn, bsq.BSQ_ERR_INVALID)
 
 
-def _dev(fn, *tensors):
-    """Every tensor given lives on the current CUDA device (where the call is enqueued)."""
-    d = torch.cuda.current_device()
-    for t in tensors:
-        _need(fn, t is None or (t.is_cuda and t.get_device() == d))
+def _arr(fn, t, dtype, n, dev):
+    """t is a contiguous tensor of n elements of this type on device dev (the current one)."""
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(fn)
 
 
-def _arr(fn, t, dtype, *shape):
-    """t is None or a contiguous tensor of this type and shape."""
-    _need(fn, t is None or (t.dtype == dtype and t.shape == shape and t.is_contiguous()))
-
-
-def _mat(fn, t, dtype, rows, cols):
+def _mat(fn, t, dtype, rows, cols, dev):
     """t is a row-major [rows, cols] matrix; returns its leading dimension."""
-    _need(fn, t.dtype == dtype and t.shape == (rows, cols) and (cols <= 1 or t.stride(1) == 1))
-    return t.stride(0) if rows > 1 else max(t.stride(0), -(-cols // 8) * 8)
+    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev:
+        _refuse(fn)
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        _refuse(fn)
+    return ld if rows > 1 else max(ld, -(-cols // 8) * 8)
 
 
 class MoeRoute(NamedTuple):
@@ -278,9 +276,12 @@ def moe_route(logits, topk, token_mask=None, renorm=True, balance_coef=None, out
     them needs T * topk + 127 * min(E, T * topk) rows at most (each expert's
     rows pad to 128)."""
     fn = "moe_route"
-    _need(fn, logits.dim() == 2 and logits.dtype in (torch.float32, torch.bfloat16))
+    dev = torch.cuda.current_device()
+    dtype = logits.dtype
+    if logits.dim() != 2 or (dtype is not torch.float32 and dtype is not torch.bfloat16):
+        _refuse(fn)
     T, E = logits.shape
-    ld = _mat(fn, logits, logits.dtype, T, E)
+    ld = _mat(fn, logits, dtype, T, E, dev)
     with_loss = balance_coef is not None
     if out is None:
         i32 = dict(dtype=torch.int32, device=logits.device)
@@ -291,26 +292,29 @@ def moe_route(logits, topk, token_mask=None, renorm=True, balance_coef=None, out
                        torch.empty(1, **f32) if with_loss else None)
     else:
         out = MoeRoute(*out)
-        _arr(fn, out.expert_ids, torch.int32, T, topk)
-        _arr(fn, out.weights, torch.float32, T, topk)
-        _arr(fn, out.rows, torch.int32, T, topk)
-        _arr(fn, out.row_index, torch.int32, T * topk)
-        for t in (out.row_offsets, out.sf_row_offsets, out.counts):
-            _arr(fn, t, torch.int32, E + 1)
-        _arr(fn, out.prob_sums, torch.float32, E)
-        _arr(fn, out.loss, torch.float32, 1)
-        _need(fn, with_loss or out.loss is None)
+        ids, weights, rows, row_index, row_offsets, sf_row_offsets, counts, prob_sums, loss = out
+        n, i32 = T * topk, torch.int32
+        _arr(fn, ids, i32, n, dev)
+        _arr(fn, weights, torch.float32, n, dev)
+        _arr(fn, rows, i32, n, dev)
+        _arr(fn, row_index, i32, n, dev)
+        _arr(fn, row_offsets, i32, E + 1, dev)
+        _arr(fn, sf_row_offsets, i32, E + 1, dev)
+        _arr(fn, counts, i32, E + 1, dev)
+        if prob_sums is not None:
+            _arr(fn, prob_sums, torch.float32, E, dev)
+        if loss is not None:
+            _arr(fn, loss, torch.float32, 1, dev)
+            if not with_loss:
+                _refuse(fn)
     if token_mask is not None:
-        _need(fn, token_mask.dtype in (torch.uint8, torch.bool) and token_mask.shape == (T,) and
-              token_mask.is_contiguous())
+        _arr(fn, token_mask, torch.bool if token_mask.dtype is torch.bool else torch.uint8, T, dev)
     if workspace is None:
         workspace = torch.empty(bsq.bsq_moe_route_workspace(T, E), dtype=torch.uint8, device=logits.device)
-    _need(fn, workspace.dtype == torch.uint8 and workspace.is_contiguous())
-    _dev(fn, logits, token_mask, workspace, *out)
-    bsq.bsq_moe_route(logits, bsq.BSQ_OUT_F32 if logits.dtype == torch.float32 else bsq.BSQ_OUT_BF16, T, E, ld,
-                      token_mask, topk, renorm, out.expert_ids, out.weights, out.rows, out.row_index, out.row_offsets,
-                      out.sf_row_offsets, out.counts, out.prob_sums, balance_coef if with_loss else 0.0, out.loss,
-                      workspace, workspace.numel())
+    nbytes = workspace.numel()
+    _arr(fn, workspace, torch.uint8, nbytes, dev)
+    bsq.bsq_moe_route(logits, bsq.BSQ_OUT_F32 if dtype is torch.float32 else bsq.BSQ_OUT_BF16, T, E, ld, token_mask,
+                      topk, renorm, *out[:8], balance_coef if with_loss else 0.0, out[8], workspace, nbytes)
     return out
 
 
@@ -319,21 +323,27 @@ def moe_route_bwd(logits, expert_ids, weights, dweights=None, counts=None, dloss
     """Gradient of the logits from the weights' gradient (fp32 [T, k]) and the
     balance loss's (fp32 [1], with the router's counts and its balance_coef)."""
     fn = "moe_route_bwd"
-    _need(fn, logits.dim() == 2 and logits.dtype in (torch.float32, torch.bfloat16) and expert_ids.dim() == 2)
+    dev = torch.cuda.current_device()
+    dtype = logits.dtype
+    if logits.dim() != 2 or (dtype is not torch.float32 and dtype is not torch.bfloat16) or expert_ids.dim() != 2:
+        _refuse(fn)
     T, E = logits.shape
     k = expert_ids.shape[1]
-    ld = _mat(fn, logits, logits.dtype, T, E)
-    _arr(fn, expert_ids, torch.int32, T, k)
-    _arr(fn, weights, torch.float32, T, k)
-    _arr(fn, dweights, torch.float32, T, k)
-    _arr(fn, counts, torch.int32, E + 1)
-    _need(fn, dloss is None or (dloss.dtype == torch.float32 and dloss.numel() == 1))
+    n = T * k
+    ld = _mat(fn, logits, dtype, T, E, dev)
+    _arr(fn, expert_ids, torch.int32, n, dev)
+    _arr(fn, weights, torch.float32, n, dev)
+    if dweights is not None:
+        _arr(fn, dweights, torch.float32, n, dev)
+    if counts is not None:
+        _arr(fn, counts, torch.int32, E + 1, dev)
+    if dloss is not None:
+        _arr(fn, dloss, torch.float32, 1, dev)
     if out is None:
-        out = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
-    ldd = _mat(fn, out, logits.dtype, T, E)
-    _dev(fn, logits, expert_ids, weights, dweights, counts, dloss, out)
-    bsq.bsq_moe_route_bwd(logits, bsq.BSQ_OUT_F32 if logits.dtype == torch.float32 else bsq.BSQ_OUT_BF16, T, E, ld, k,
-                          renorm, expert_ids, weights, dweights, counts, balance_coef, dloss, out, ldd)
+        out = torch.empty(T, E, dtype=dtype, device=logits.device)
+    ldd = _mat(fn, out, dtype, T, E, dev)
+    bsq.bsq_moe_route_bwd(logits, bsq.BSQ_OUT_F32 if dtype is torch.float32 else bsq.BSQ_OUT_BF16, T, E, ld, k, renorm,
+                          expert_ids, weights, dweights, counts, balance_coef, dloss, out, ldd)
     return out
 
 
@@ -341,16 +351,18 @@ def moe_combine(y, rows, weights=None, out=None):
     """Per token: the weighted sum of its rows of y [R, H] (bf16), bf16
     [T, H].  rows int32 [T, k] (-1: none), weights fp32 [T, k] or None for 1."""
     fn = "moe_combine"
-    _need(fn, y.dim() == 2 and rows.dim() == 2)
+    dev = torch.cuda.current_device()
+    if y.dim() != 2 or rows.dim() != 2:
+        _refuse(fn)
     R, H = y.shape
     T, k = rows.shape
-    ldy = _mat(fn, y, torch.bfloat16, R, H)
-    _arr(fn, rows, torch.int32, T, k)
-    _arr(fn, weights, torch.float32, T, k)
+    ldy = _mat(fn, y, torch.bfloat16, R, H, dev)
+    _arr(fn, rows, torch.int32, T * k, dev)
+    if weights is not None:
+        _arr(fn, weights, torch.float32, T * k, dev)
     if out is None:
         out = torch.empty(T, H, dtype=torch.bfloat16, device=y.device)
-    ldo = _mat(fn, out, torch.bfloat16, T, H)
-    _dev(fn, y, rows, weights, out)
+    ldo = _mat(fn, out, torch.bfloat16, T, H, dev)
     bsq.bsq_moe_combine(y, R, H, ldy, rows, weights, T, k, out, ldo)
     return out
 
@@ -360,32 +372,40 @@ def moe_combine_bwd(dout, y, rows, weights, out=None):
     the bf16 [R, H], or the MXFP8 pair (codes [R, H], sf) it was kept as.
     Without out, the rows of dy that no token has are zeros."""
     fn = "moe_combine_bwd"
+    dev = torch.cuda.current_device()
     codes = sf = None
     if isinstance(y, (tuple, list)):
         codes, sf = y
         y = None
     kept = y if codes is None else codes
-    _need(fn, kept.dim() == 2 and rows.dim() == 2)
+    if kept.dim() != 2 or rows.dim() != 2:
+        _refuse(fn)
     R, H = kept.shape
     T, k = rows.shape
     ldy = H
     if codes is None:
-        ldy = _mat(fn, y, torch.bfloat16, R, H)
+        ldy = _mat(fn, y, torch.bfloat16, R, H, dev)
     else:
-        _arr(fn, codes, torch.uint8, R, H)
-        _need(fn, sf.dtype == torch.uint8 and sf.is_contiguous() and sf.numel() >= sf_bytes(R, H // 32))
-    ldo = _mat(fn, dout, torch.bfloat16, T, H)
-    _arr(fn, rows, torch.int32, T, k)
-    _arr(fn, weights, torch.float32, T, k)
+        _arr(fn, codes, torch.uint8, R * H, dev)
+        _scales(fn, sf, R, H // 32, dev)
+    ldo = _mat(fn, dout, torch.bfloat16, T, H, dev)
+    _arr(fn, rows, torch.int32, T * k, dev)
+    _arr(fn, weights, torch.float32, T * k, dev)
     if out is None:
         out = (torch.zeros(R, H, dtype=torch.bfloat16, device=dout.device),
                torch.empty(T, k, dtype=torch.float32, device=dout.device))
     dy, dweights = out
-    lddy = _mat(fn, dy, torch.bfloat16, R, H)
-    _arr(fn, dweights, torch.float32, T, k)
-    _dev(fn, dout, y, codes, sf, rows, weights, dy, dweights)
+    lddy = _mat(fn, dy, torch.bfloat16, R, H, dev)
+    _arr(fn, dweights, torch.float32, T * k, dev)
     bsq.bsq_moe_combine_bwd(dout, ldo, y, ldy, codes, sf, R, H, rows, weights, T, k, dy, lddy, dweights)
     return dy, dweights
+
+
+def _scales(fn, sf, rows, nblocks, dev):
+    """sf is a swizzled scale-factor buffer for at least this many rows."""
+    _arr(fn, sf, torch.uint8, sf.numel(), dev)
+    if sf.numel() < -(-rows // 128) * 128 * (-(-nblocks // 4) * 4):
+        _refuse(fn)
 
 
 def swiglu_ckpt(u, n_rows=None, amax=True, out=None):
@@ -393,22 +413,24 @@ def swiglu_ckpt(u, n_rows=None, amax=True, out=None):
     the backward pass: (h [M, F] bf16, codes [M, 2F], sf swizzled, amax [1] of
     h or None).  n_rows int32 [1]: only that many rows exist."""
     fn = "swiglu_ckpt"
-    _need(fn, u.dim() == 2 and u.shape[1] % 2 == 0)
+    dev = torch.cuda.current_device()
+    if u.dim() != 2 or u.shape[1] % 2:
+        _refuse(fn)
     M, F = u.shape[0], u.shape[1] // 2
-    ldu = _mat(fn, u, torch.bfloat16, M, 2 * F)
-    nb = sf_bytes(M, F // 16)
+    ldu = _mat(fn, u, torch.bfloat16, M, 2 * F, dev)
     if out is None:
         out = (torch.empty(M, F, dtype=torch.bfloat16, device=u.device),
                torch.empty(M, 2 * F, dtype=torch.uint8, device=u.device),
-               torch.zeros(nb, dtype=torch.uint8, device=u.device),
+               torch.zeros(sf_bytes(M, F // 16), dtype=torch.uint8, device=u.device),
                torch.empty(1, dtype=torch.float32, device=u.device) if amax else None)
     h, codes, sf, am = out
-    ldh = _mat(fn, h, torch.bfloat16, M, F)
-    _arr(fn, codes, torch.uint8, M, 2 * F)
-    _need(fn, sf.dtype == torch.uint8 and sf.is_contiguous() and sf.numel() >= nb)
-    _arr(fn, am, torch.float32, 1)
-    _need(fn, n_rows is None or (n_rows.dtype == torch.int32 and n_rows.numel() == 1))
-    _dev(fn, u, n_rows, h, codes, sf, am)
+    ldh = _mat(fn, h, torch.bfloat16, M, F, dev)
+    _arr(fn, codes, torch.uint8, M * 2 * F, dev)
+    _scales(fn, sf, M, F // 16, dev)
+    if am is not None:
+        _arr(fn, am, torch.float32, 1, dev)
+    if n_rows is not None:
+        _arr(fn, n_rows, torch.int32, 1, dev)
     bsq.bsq_swiglu_ckpt(u, M, F, ldu, n_rows, h, ldh, codes, sf, am)
     return h, codes, sf, am
 
@@ -417,18 +439,20 @@ def swiglu_ckpt_bwd(dh, codes, sf, n_rows=None, recompute_h=False, out=None):
     """Gradient of swiglu_ckpt's u from dh [M, F] (bf16) and the checkpoint:
     (du [M, 2F] bf16, h [M, F] bf16 formed again from the checkpoint, or None)."""
     fn = "swiglu_ckpt_bwd"
-    _need(fn, dh.dim() == 2)
+    dev = torch.cuda.current_device()
+    if dh.dim() != 2:
+        _refuse(fn)
     M, F = dh.shape
-    lddh = _mat(fn, dh, torch.bfloat16, M, F)
-    _arr(fn, codes, torch.uint8, M, 2 * F)
-    _need(fn, sf.dtype == torch.uint8 and sf.is_contiguous() and sf.numel() >= sf_bytes(M, F // 16))
-    _need(fn, n_rows is None or (n_rows.dtype == torch.int32 and n_rows.numel() == 1))
+    lddh = _mat(fn, dh, torch.bfloat16, M, F, dev)
+    _arr(fn, codes, torch.uint8, M * 2 * F, dev)
+    _scales(fn, sf, M, F // 16, dev)
+    if n_rows is not None:
+        _arr(fn, n_rows, torch.int32, 1, dev)
     if out is None:
         out = (torch.empty(M, 2 * F, dtype=torch.bfloat16, device=dh.device),
                torch.empty(M, F, dtype=torch.bfloat16, device=dh.device) if recompute_h else None)
     du, h = out
-    lddu = _mat(fn, du, torch.bfloat16, M, 2 * F)
-    ldh = _mat(fn, h, torch.bfloat16, M, F) if h is not None else 0
-    _dev(fn, dh, codes, sf, n_rows, du, h)
+    lddu = _mat(fn, du, torch.bfloat16, M, 2 * F, dev)
+    ldh = _mat(fn, h, torch.bfloat16, M, F, dev) if h is not None else 0
     bsq.bsq_swiglu_ckpt_bwd(dh, lddh, codes, sf, M, F, n_rows, du, lddu, h, ldh)
     return du, h
