@@ -110,6 +110,11 @@ struct Row<uint16_t, LPT, Q> {
             }
         }
     }
+    BSQ_DEV float quad_max(int q) const {
+        uint32_t m;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w[q].x), "r"(w[q].y));
+        return fmaxf(bf16_lo(m), bf16_hi(m));
+    }
     BSQ_DEV void get(int q, float z[4]) const {
         z[0] = bf16_lo(w[q].x);
         z[1] = bf16_hi(w[q].x);
@@ -136,6 +141,9 @@ struct Row<float, LPT, Q> {
                 if (e + 3 < E) w[q].w = __ldg(row + e + 3);
             }
         }
+    }
+    BSQ_DEV float quad_max(int q) const {
+        return fmaxf(fmaxf(w[q].x, w[q].y), fmaxf(w[q].z, w[q].w));
     }
     BSQ_DEV void get(int q, float z[4]) const {
         z[0] = w[q].x;
@@ -359,13 +367,73 @@ BSQ_DEV void best_list(const Row<In, LPT, Q> &row, int sub, uint32_t bits, float
     }
 }
 
+// The same for many logits per lane, in two steps: the L quads with the best
+// maxima hold the L best logits (a quad before which L others come has L
+// logits before each of its own), so lists of quads come first, then lane i
+// reads quad i's four logits again, and lists are made of those.  Five and
+// more quads a lane: 131072x256, k = 8, then takes 71 us instead of 77.  The
+// list is that of the lanes sub < L alone.
+template <int L, typename In, int LPT, int Q>
+BSQ_DEV void best_of_quads(const Row<In, LPT, Q> &row, const In *logits, int sub, int E, bool vec, uint32_t bits,
+                           float v[L]) {
+    const uint32_t qbits = expert_bits<In>((E + 3) >> 2);
+#pragma unroll
+    for (int q0 = 0; q0 < Q; q0 += L) {
+        float w[L];
+#pragma unroll
+        for (int i = 0; i < L; i++)
+            w[i] = q0 + i < Q ? with_expert(row.quad_max(q0 + i), (uint32_t)((q0 + i) * LPT + sub), qbits) : -INFINITY;
+        sort_desc<L>(w);
+        if (q0 == 0) {
+#pragma unroll
+            for (int i = 0; i < L; i++) v[i] = w[i];
+        } else {
+            keep_best<L>(v, w);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < LPT; o <<= 1) {
+        float w[L];
+#pragma unroll
+        for (int i = 0; i < L; i++) w[i] = __shfl_xor_sync(kFull, v[i], o);
+        keep_best<L>(v, w);
+    }
+    const float mine = entry<L>(v, sub);
+    const bool some = sub < L && mine > -INFINITY;
+    const int quad = some ? expert_of(__float_as_uint(mine), qbits) : 0;
+    Row<In, 1, 1> one;
+    one.load(logits + 4 * quad, E - 4 * quad, 0, vec, some);
+    float z[4];
+    one.get(0, z);
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = with_expert(z[i], (uint32_t)(4 * quad + i), bits);
+    sort_desc<4>(v);
+    if (L == 8) {  // two lists of four make one of eight
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[L - 1 - i] = __shfl_xor_sync(kFull, v[i], 1);
+#pragma unroll
+        for (int h = L / 2; h; h >>= 1)
+#pragma unroll
+            for (int i = 0; i < L; i++)
+                if (!(i & h)) order2(v[i], v[i + h]);
+    }
+#pragma unroll
+    for (int o = L / 4; o < L; o <<= 1) {
+        float w[L];
+#pragma unroll
+        for (int i = 0; i < L; i++) w[i] = __shfl_xor_sync(kFull, v[i], o);
+        keep_best<L>(v, w);
+    }
+}
+
 // Slot `sub` of the token by such a list: its expert (-1: none) and logit.
 // False where the order is not certain.
 template <int L, typename In, int LPT, int Q>
-BSQ_DEV bool choose(const Row<In, LPT, Q> &row, const In *logits, int sub, int E, int k, int &e, float &z) {
+BSQ_DEV bool choose(const Row<In, LPT, Q> &row, const In *logits, int sub, int E, bool vec, int k, int &e, float &z) {
     const uint32_t bits = expert_bits<In>(E);
     float v[L];
-    best_list<L>(row, sub, bits, v);
+    if (Q >= 5) best_of_quads<L>(row, logits, sub, E, vec, bits, v);
+    else best_list<L>(row, sub, bits, v);
     const float mine = entry<L>(v, sub);
     const uint32_t b = __float_as_uint(mine);
     e = sub < k && mine > -INFINITY ? expert_of(b, bits) : -1;
@@ -377,7 +445,7 @@ BSQ_DEV bool choose(const Row<In, LPT, Q> &row, const In *logits, int sub, int E
     const uint32_t next = __shfl_down_sync(kFull, b, 1, LPT);
     bool bad = sub + 1 < k && e >= 0 && ((b ^ next) & ~bits) == 0;
     // the last slot's truncated logit: nothing else may have it
-    const float last = entry<L>(v, k - 1);
+    const float last = __shfl_sync(kFull, entry<L>(v, k - 1), 0, LPT);
     const uint32_t lb = __float_as_uint(last);
     const float floor = __uint_as_float((lb >> 31) ? lb | bits : lb & ~bits);
     int n = 0;
@@ -443,8 +511,8 @@ template <typename In, int LPT, int Q, int L>
 __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                          int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
                                                          int renorm, int want_p, RouteOut out, int64_t nchunk,
-                                                         uint32_t *__restrict__ hist, uint8_t *__restrict__ hist8,
-                                                         float *__restrict__ psum, int64_t stride, float coef) {
+                                                         uint8_t *__restrict__ hist, float *__restrict__ psum,
+                                                         float coef) {
     grid_dependents_launch();
     grid_dependency_wait();
     extern __shared__ unsigned long long smem[];
@@ -484,7 +552,7 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
         if (L > 0) {
             int e;
             float z;
-            done = choose<L == 0 ? 4 : L>(row, logits + (t0 + tl) * ldl, sub, E, k, e, z);
+            done = choose<L == 0 ? 4 : L>(row, logits + (t0 + tl) * ldl, sub, E, vec, k, e, z);
             if (done) {  // the same for the whole warp
                 top = __shfl_sync(kFull, e >= 0 ? z : 0.0f, lane & ~(LPT - 1));
                 const float x = e >= 0 ? ex2((z - top) * kLog2e) : 0.0f;
@@ -567,17 +635,14 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
         for (int e = threadIdx.x; e <= E; e += blockDim.x) {
             const unsigned long long m = smem[e];
             const uint32_t n = (uint32_t)__popcll(m), first = m ? (uint32_t)(__ffsll(m) - 1) : 0u;
-            if (hist8) {  // a row of counts and a row of first tokens per chunk
-                uint8_t *to = hist8 + (int64_t)blockIdx.x * 2 * hist_row(E);
-                to[e] = (uint8_t)n;
-                to[hist_row(E) + e] = (uint8_t)first;
-            } else {  // a row per expert: count in the low byte, first token above it
-                hist[(int64_t)e * stride + blockIdx.x] = n | first << 8;
-            }
+            // a row of counts and a row of first tokens per chunk
+            uint8_t *to = hist + (int64_t)blockIdx.x * 2 * hist_row(E);
+            to[e] = (uint8_t)n;
+            to[hist_row(E) + e] = (uint8_t)first;
             if (want_p && e < E) {
                 float v = 0.0f;
                 for (int w = 0; w < nwarps; w++) v += red[w * E + e];
-                psum[hist8 ? (int64_t)blockIdx.x * E + e : (int64_t)e * stride + blockIdx.x] = v;
+                psum[(int64_t)blockIdx.x * E + e] = v;
             }
         }
     } else {
@@ -613,197 +678,159 @@ __global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ 
     }
 }
 
-// Pass 2.  One CTA per expert (and one for the token count): its counts per
-// chunk become exclusive prefixes in place, their total goes to counts[e];
-// the first token that chose e, and the sum of its probabilities, go along.
-// A thread takes eight neighbouring chunks (rows are padded to eight).
-__global__ void __launch_bounds__(256) route_scan_kernel(uint32_t *__restrict__ hist, const float *__restrict__ psum,
-                                                         int64_t nchunk, int64_t stride, int E,
-                                                         int32_t *__restrict__ counts, int32_t *__restrict__ first,
-                                                         float *__restrict__ psum_total) {
+// Pass 2, for many chunks.  A CTA takes kBlock consecutive chunks and 32 experts
+// (row E, the tokens, among them), a lane one expert and a warp a run of the
+// chunks, all loads in flight at once: the exclusive prefix of every chunk
+// inside the block, and the block's counts and sums of probabilities.
+constexpr int kBlock = 64, kRun = kBlock / 8;
+
+__global__ void __launch_bounds__(256) route_block_kernel(const uint8_t *__restrict__ hist,
+                                                          const float *__restrict__ psum, int64_t nchunk, int E,
+                                                          uint16_t *__restrict__ prefix, int32_t *__restrict__ count,
+                                                          float *__restrict__ psum_block) {
     grid_dependents_launch();
     grid_dependency_wait();
-    __shared__ int wsum[8];
-    __shared__ float fsum[8];
-    __shared__ int sfirst;
-    const int e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t *h = hist + (int64_t)e * stride;
-    if (threadIdx.x == 0) sfirst = 0x7FFFFFFF;
-    __syncthreads();
-    int carry = 0;
-    float p = 0.0f;
-    for (int64_t c0 = 0; c0 < nchunk; c0 += 2048) {
-        const int64_t c = c0 + threadIdx.x * 8;
-        uint32_t v[8] = {};
-        if (c < nchunk) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(h + c), b = *reinterpret_cast<const uint4 *>(h + c + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-            if (psum && e < E) {
-                const float *q = psum + (int64_t)e * stride + c;
-                const float4 x = __ldg(reinterpret_cast<const float4 *>(q)), y = __ldg(reinterpret_cast<const float4 *>(q + 4));
-                const float f[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    if (c + i < nchunk) p += f[i];
-            }
-        }
-        int s = 0, low = 0x7FFFFFFF;
-#pragma unroll
-        for (int i = 7; i >= 0; i--) {
-            if (c + i >= nchunk) v[i] = 0;  // the padding was never written
-            if (v[i] & 0xFFu) low = (int)((c + i) * kChunk) + (int)(v[i] >> 8);
-            v[i] &= 0xFFu;
-            s += (int)v[i];
-        }
-        low = __reduce_min_sync(kFull, low);
-        if (lane == 0 && low != 0x7FFFFFFF) atomicMin(&sfirst, low);
-        int inc = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, inc, o);
-            if (lane >= o) inc += u;
-        }
-        if (lane == 31) wsum[warp] = inc;
-        __syncthreads();
-        int before = 0, all = 0;
-#pragma unroll
-        for (int w = 0; w < 8; w++) {
-            if (w < warp) before += wsum[w];
-            all += wsum[w];
-        }
-        if (c < nchunk) {
-            uint32_t at = (uint32_t)(carry + before + inc - s);
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint32_t n = v[i];
-                v[i] = at;
-                at += n;
-            }
-            *reinterpret_cast<uint4 *>(h + c) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4 *>(h + c + 4) = make_uint4(v[4], v[5], v[6], v[7]);
-        }
-        carry += all;
-        __syncthreads();
-    }
-    p = warp_sum(p);
-    if (lane == 0) fsum[warp] = p;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        counts[e] = carry;
-        if (e < E) {
-            first[e] = sfirst;
-            if (psum) {
-                float v = 0.0f;
-                for (int w = 0; w < 8; w++) v += fsum[w];
-                psum_total[e] = v;
-            }
-        }
-    }
-}
-
-// Exclusive scan over e < E of counts[e] (PAD128: each rounded up to 128)
-// into off[0..E], by one CTA of 256 threads holding four experts each.
-template <bool PAD128>
-BSQ_DEV void scan_counts(const int32_t *counts, int E, int32_t *off, int *wsum) {
+    __shared__ int run[8][32];
+    __shared__ float fsum[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int n[4], s = 0;
+    const int e = blockIdx.y * 32 + lane, row = hist_row(E);
+    const int64_t c = (int64_t)blockIdx.x * kBlock + warp * kRun;
+    int v[kRun], n = 0;
+    float f[kRun], p = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int e = threadIdx.x * 4 + i;
-        n[i] = e < E ? counts[e] : 0;
-        if (PAD128) n[i] = (n[i] + 127) & ~127;
-        s += n[i];
+    for (int i = 0; i < kRun; i++) {
+        v[i] = c + i < nchunk && e <= E ? __ldg(hist + (c + i) * 2 * row + e) : 0;
+        f[i] = c + i < nchunk && e < E && psum ? __ldg(psum + (c + i) * E + e) : 0.0f;
     }
-    int inc = s;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, inc, o);
-        if (lane >= o) inc += u;
+    for (int i = 0; i < kRun; i++) {
+        n += v[i];
+        p += f[i];
     }
-    if (lane == 31) wsum[warp] = inc;
+    run[warp][lane] = n;
+    fsum[warp][lane] = p;
     __syncthreads();
-    int at = inc - s;
-    for (int w = 0; w < warp; w++) at += wsum[w];
+    int at = 0;
+    for (int w = 0; w < warp; w++) at += run[w][lane];
+    if (e > E) return;
+    if (warp == 7) {
+        count[(int64_t)blockIdx.x * (E + 1) + e] = at + n;
+        if (e < E && psum) {
+            float all = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int e = threadIdx.x * 4 + i;
-        if (e <= E) off[e] = at;
-        at += n[i];
+            for (int w = 0; w < 8; w++) all += fsum[w][lane];
+            psum_block[(int64_t)blockIdx.x * E + e] = all;
+        }
     }
-    if (E == 1024 && threadIdx.x == 255) off[E] = at;
-    __syncthreads();
+    if (e == E) return;
+#pragma unroll
+    for (int i = 0; i < kRun; i++) {
+        if (c + i < nchunk) prefix[(c + i) * E + e] = (uint16_t)at;  // 64 chunks of 64 tokens
+        at += v[i];
+    }
 }
 
-// Pass 3.  Row of a slot = its expert's offset + the chunk's prefix + the
-// rank inside the chunk; the rows past the last routed one repeat the first
-// row's token.  CTA 0 also writes the offsets and the loss.
-__global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ rows,
-                                                          uint32_t n, UnitDiv k, int E, int64_t stride,
-                                                          const uint32_t *__restrict__ hist,
-                                                          const int32_t *__restrict__ counts,
-                                                          const int32_t *__restrict__ first,
-                                                          const float *__restrict__ psum_total, float coef,
-                                                          int32_t *__restrict__ row_index,
-                                                          int32_t *__restrict__ row_off,
-                                                          int32_t *__restrict__ sf_row_off,
-                                                          float *__restrict__ prob_sums, float *__restrict__ loss) {
+// Sum over b0 <= b < b1 of p[b * stride], 16 loads in flight.
+template <typename V>
+BSQ_DEV V column_sum(const V *p, int64_t stride, int64_t b0, int64_t b1) {
+    V s = 0;
+    for (int64_t b = b0; b < b1; b += 16) {
+        V v[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) v[i] = b + i < b1 ? __ldg(p + (b + i) * stride) : V(0);
+#pragma unroll
+        for (int i = 0; i < 16; i++) s += v[i];
+    }
+    return s;
+}
+
+// Pass 3.  Row of a slot = its expert's offset + the prefix of the blocks
+// before + the chunk's prefix in its block + the rank inside the chunk; the
+// rows past the last routed one repeat the first row's token.  A CTA takes
+// `span` chunks of one block; the last one also writes the offsets and the loss.
+__global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd, int E, int64_t nchunk, int span,
+                                                          const uint8_t *__restrict__ hist,
+                                                          const uint16_t *__restrict__ prefix,
+                                                          const int32_t *__restrict__ count,
+                                                          const float *__restrict__ psum_block, RouteOut out,
+                                                          float coef) {
+    grid_dependents_launch();
     grid_dependency_wait();
-    __shared__ int32_t off[kRouteMaxExperts + 1];
-    __shared__ int wsum[8];
-    __shared__ int first_token;
-    if (threadIdx.x == 0) first_token = 0;
-    scan_counts<false>(counts, E, off, wsum);
-    for (int e = threadIdx.x; e < E; e += 256)
-        if (off[e] == 0 && off[e + 1] > 0) first_token = first[e];  // one expert only
+    __shared__ int32_t base[kRouteMaxExperts + 1], all[kRouteMaxExperts + 1], off[kRouteMaxExperts + 1];
+    __shared__ float sums[kRouteMaxExperts];
+    __shared__ int first_chunk;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t blocks = gridDim.x, b = blockIdx.x;
+    const int64_t c0 = b * kBlock + blockIdx.y * span, c1 = min(min(c0 + span, (b + 1) * kBlock), nchunk);
+    for (int e = threadIdx.x; e <= E; e += 256) {
+        const int before = column_sum(count + e, E + 1, 0, b);
+        base[e] = before;
+        all[e] = before + column_sum(count + e, E + 1, b, blocks);
+    }
     __syncthreads();
-    const uint32_t total = (uint32_t)off[E];
-    // four slots at a time, so that their loads overlap (n < 2^31)
-    for (uint32_t i0 = blockIdx.x * 1024 + threadIdx.x; i0 < n; i0 += gridDim.x * 1024) {
+    if (warp == 0) warp_scan<false>([&](int e) { return all[e]; }, E, off);
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += 256) base[e] += off[e];
+    __syncthreads();
+    const uint32_t total = (uint32_t)off[E], k = kd.d;
+    const uint32_t i1 = (uint32_t)(min(c1 * kChunk, T) * k);  // below 2^31
+    // four slots at a time, so that their loads overlap
+    for (uint32_t i0 = (uint32_t)(c0 * kChunk * k) + threadIdx.x; i0 < i1; i0 += 1024) {
         int e[4], r[4];
 #pragma unroll
         for (int u = 0; u < 4; u++) {
             const uint32_t i = i0 + 256 * u;
-            e[u] = i < n ? __ldg(ids + i) : -1;
-            r[u] = i < n ? rows[i] : 0;
+            e[u] = i < i1 ? __ldg(out.ids + i) : -1;
+            r[u] = i < i1 ? out.rows[i] : 0;
         }
 #pragma unroll
         for (int u = 0; u < 4; u++)
             if (e[u] >= 0)
-                r[u] += off[e[u]] + (int)__ldg(hist + (int64_t)e[u] * stride + divide(i0 + 256 * u, k) / kChunk);
+                r[u] += base[e[u]] + (int)__ldg(prefix + (int64_t)(divide(i0 + 256 * u, kd) / kChunk) * E + e[u]);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
             const uint32_t i = i0 + 256 * u;
             if (e[u] >= 0) {
-                rows[i] = r[u];
-                row_index[r[u]] = (int32_t)divide(i, k);
+                out.rows[i] = r[u];
+                out.row_index[r[u]] = (int32_t)divide(i, kd);
             }
-            if (i < n && i >= total) row_index[i] = first_token;
         }
     }
-    if (blockIdx.x == 0) {
-        for (int e = threadIdx.x; e <= E; e += 256) row_off[e] = off[e];
-        float part = 0.0f;
-        if (psum_total)
-            for (int e = threadIdx.x; e < E; e += 256) {
-                const float p = psum_total[e];
-                if (prob_sums) prob_sums[e] = p;
-                part += (float)counts[e] * p;
-            }
-        __syncthreads();
-        if (loss) {
-            __shared__ float fsum[8];
-            part = warp_sum(part);
-            if ((threadIdx.x & 31) == 0) fsum[threadIdx.x >> 5] = part;
+    if (c0 < c1 && i1 > total) {
+        int token = 0;
+        if (total > 0) {  // the first chunk that has the first row's expert, and its first token there
+            int e0 = 0;
+            while (off[e0 + 1] == 0) e0++;
+            int64_t b0 = 0;
+            while (__ldg(count + b0 * (E + 1) + e0) == 0) b0++;
+            if (threadIdx.x == 0) first_chunk = kBlock;
             __syncthreads();
-            if (threadIdx.x == 0) {
-                float v = 0.0f;
-                for (int w = 0; w < 8; w++) v += fsum[w];
-                *loss = balance_loss(v, counts[E], coef, E, (int)k.d);
-            }
+            if (threadIdx.x < kBlock && b0 * kBlock + threadIdx.x < nchunk &&
+                __ldg(hist + (b0 * kBlock + threadIdx.x) * 2 * hist_row(E) + e0))
+                atomicMin(&first_chunk, (int)threadIdx.x);
+            __syncthreads();
+            const int64_t c = b0 * kBlock + first_chunk;
+            token = (int)(c * kChunk) + __ldg(hist + c * 2 * hist_row(E) + hist_row(E) + e0);
         }
-        scan_counts<true>(counts, E, off, wsum);
-        for (int e = threadIdx.x; e <= E; e += 256) sf_row_off[e] = off[e];
+        for (uint32_t i = max((uint32_t)(c0 * kChunk * k), total) + threadIdx.x; i < i1; i += 256)
+            out.row_index[i] = token;
+    }
+    if (b < blocks - 1 || blockIdx.y < gridDim.y - 1) return;
+    for (int e = threadIdx.x; e <= E; e += 256) {
+        out.counts[e] = all[e];
+        out.row_off[e] = off[e];
+        if (psum_block && e < E) {
+            sums[e] = column_sum(psum_block + e, E, 0, blocks);
+            if (out.prob_sums) out.prob_sums[e] = sums[e];
+        }
+    }
+    __syncthreads();
+    if (warp == 0) warp_scan<true>([&](int e) { return all[e]; }, E, out.sf_row_off);
+    if (warp == 1 && out.loss) {
+        float v = 0.0f;
+        for (int e = lane; e < E; e += 32) v += (float)all[e] * sums[e];
+        v = warp_sum(v);
+        if (lane == 0) *out.loss = balance_loss(v, all[E], coef, E, (int)k);
     }
 }
 
@@ -816,7 +843,7 @@ __global__ void __launch_bounds__(256) route_place_kernel(const int32_t *__restr
 constexpr int kSmallHist = 48 * 1024, kSmallChunks = 512;
 
 __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDiv kd, int E, int nchunk,
-                                                               UnitDiv wd, const uint8_t *__restrict__ hist8,
+                                                               UnitDiv wd, const uint8_t *__restrict__ hist,
                                                                const float *__restrict__ psum, RouteOut out,
                                                                float coef) {
     grid_dependents_launch();
@@ -868,7 +895,7 @@ __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDi
     for (int u = threadIdx.x; u < words * parts; u += 256) {
         const int part = (int)divide((uint32_t)u, wd), w = u - part * words;
         auto add_up = [&](int c0, int c1, int32_t *to) {
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(hist8) + w;
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(hist) + w;
             uint32_t even = 0, odd = 0;
             int c = c0 + part;
 #pragma unroll 2
@@ -908,12 +935,12 @@ __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDi
             int e0 = 0;
             while (off[e0 + 1] == 0) e0++;
             for (int c = threadIdx.x; c < nchunk; c += 256)
-                if (hist8[c * 2 * row + e0]) {
+                if (hist[c * 2 * row + e0]) {
                     atomicMin(&first_chunk, c);
                     break;
                 }
             __syncthreads();
-            token = first_chunk * kChunk + hist8[first_chunk * 2 * row + row + e0];
+            token = first_chunk * kChunk + hist[first_chunk * 2 * row + row + e0];
         }
         for (int j = threadIdx.x; j < here; j += 256)
             if ((int)slot0 + j >= total) out.row_index[slot0 + j] = token;
@@ -1388,9 +1415,7 @@ struct TopkLaunch {
         return launch_dependent(
                    kern, dim3((unsigned)w.nchunk), dim3(threads), smem, s, static_cast<const In *>(a.logits), a.T, E,
                    a.ldl, (int)quads<In>(a.logits, E, a.ldl), a.mask, unit_div((uint32_t)k), (int)a.renorm, want_p, out,
-                   w.nchunk, reinterpret_cast<uint32_t *>(a.ws + w.hist),
-                   small_hist(w.nchunk, E) ? a.ws + w.hist : (uint8_t *)nullptr,
-                   reinterpret_cast<float *>(a.ws + w.psum), w.stride, a.coef) != cudaSuccess;
+                   w.nchunk, a.ws + w.hist, reinterpret_cast<float *>(a.ws + w.psum), a.coef) != cudaSuccess;
     }
 };
 
@@ -1416,12 +1441,13 @@ struct BwdLaunch {
 RouteWorkspace route_workspace(int64_t T, int64_t E) {
     RouteWorkspace w;
     w.nchunk = std::max<int64_t>((T + kChunk - 1) / kChunk, 1);
-    w.stride = up(w.nchunk, 8);
+    const int64_t blocks = (w.nchunk + kBlock - 1) / kBlock;
     w.hist = 0;
-    w.psum = up(w.hist + 4 * (E + 1) * w.stride, 256);
-    w.first = up(w.psum + 4 * E * w.stride, 256);
-    w.psum_total = up(w.first + 4 * E, 256);
-    w.bytes = up(w.psum_total + 4 * E, 256);
+    w.prefix = up(w.nchunk * 2 * hist_row((int)E), 256);
+    w.psum = up(w.prefix + 2 * E * w.nchunk, 256);
+    w.count = up(w.psum + 4 * E * w.nchunk, 256);
+    w.psum_block = up(w.count + 4 * (E + 1) * blocks, 256);
+    w.bytes = up(w.psum_block + 4 * E * blocks, 256);
     return w;
 }
 
@@ -1433,28 +1459,28 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
         return 1;
     if (w.nchunk == 1) return 0;
     const int E = (int)a.E;
-    uint32_t *hist = reinterpret_cast<uint32_t *>(a.ws + w.hist);
-    int32_t *first = reinterpret_cast<int32_t *>(a.ws + w.first);
     float *psum = want_p ? reinterpret_cast<float *>(a.ws + w.psum) : nullptr;
-    float *total = want_p ? reinterpret_cast<float *>(a.ws + w.psum_total) : nullptr;
-    if (small_hist(w.nchunk, E)) {
-        const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
-                           a.loss};
+    const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums, a.loss};
+    if (small_hist(w.nchunk, E))
         return launch_dependent(route_scan_place_kernel, dim3((unsigned)w.nchunk + 1), dim3(256), 0, s, a.T,
                                 unit_div((uint32_t)a.topk), E, (int)w.nchunk,
-                                unit_div((uint32_t)hist_row(E) / 4), (const uint8_t *)(a.ws + w.hist), (const float *)psum, out, a.coef) != cudaSuccess;
-    }
-    if (launch_dependent(route_scan_kernel, dim3(E + 1), dim3(256), 0, s, hist, (const float *)psum, w.nchunk,
-                         w.stride, E, a.counts, first, total) != cudaSuccess)
+                                unit_div((uint32_t)hist_row(E) / 4), (const uint8_t *)(a.ws + w.hist), (const float *)psum, out,
+                                a.coef) != cudaSuccess;
+    const int64_t blocks = (w.nchunk + kBlock - 1) / kBlock;
+    uint16_t *prefix = reinterpret_cast<uint16_t *>(a.ws + w.prefix);
+    int32_t *count = reinterpret_cast<int32_t *>(a.ws + w.count);
+    float *psum_block = want_p ? reinterpret_cast<float *>(a.ws + w.psum_block) : nullptr;
+    if (launch_dependent(route_block_kernel, dim3((unsigned)blocks, E / 32 + 1), dim3(256), 0, s,
+                         (const uint8_t *)(a.ws + w.hist), (const float *)psum, w.nchunk, E, prefix, count,
+                         psum_block) != cudaSuccess)
         return 1;
-    const int64_t n = a.T * a.topk;
-    const unsigned grid = (unsigned)std::min<int64_t>((n + 1023) / 1024, (int64_t)num_sms * 8);
-    if (launch_dependent(route_place_kernel, dim3(grid), dim3(256), 0, s, (const int32_t *)a.ids, a.rows, (uint32_t)n,
-                         unit_div((uint32_t)a.topk), E, w.stride, (const uint32_t *)hist, (const int32_t *)a.counts, (const int32_t *)first,
-                         (const float *)total, a.coef, a.row_index, a.row_off, a.sf_row_off, a.prob_sums,
-                         a.loss) != cudaSuccess)
-        return 1;
-    return launched();
+    // about three CTAs per SM: each adds up all blocks' counts
+    const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(kBlock, 3 * num_sms / blocks));
+    const int span = (kBlock + parts - 1) / parts;
+    return launch_dependent(route_place_kernel, dim3((unsigned)blocks, (kBlock + span - 1) / span), dim3(256), 0, s,
+                            a.T, unit_div((uint32_t)a.topk), E, w.nchunk, span, (const uint8_t *)(a.ws + w.hist),
+                            (const uint16_t *)prefix, (const int32_t *)count, (const float *)psum_block, out,
+                            a.coef) != cudaSuccess;
 }
 
 int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {

@@ -10,7 +10,7 @@ constexpr int kRouteMaxTopk = 32;       // one slot per lane of a warp
 
 // Byte offsets of the router's workspace (moe.cu explains its use).
 struct RouteWorkspace {
-    int64_t nchunk, stride, hist, psum, first, psum_total, bytes;
+    int64_t nchunk, hist, prefix, psum, count, psum_block, bytes;
 };
 RouteWorkspace route_workspace(int64_t T, int64_t E);
 

@@ -63,8 +63,8 @@ def check_route(r, z, k, mask, renorm, coef):
     rel = (3 * ref.spread(n64(z), want["live"]) + 4 + -(-E // 32) + 5 + 3) * U
     within(n64(r.weights), want["weights"], rel * want["weights"] + TINY, "weights")
     if coef is not None:
-        # the tokens of a warp, the warps, the chunks of a thread, two trees, then the loss's own steps
-        rel += (8 + 8 + T / 64 / 256 + 16) * U
+        # the tokens of a warp, the warps, the chunks, a tree, then the loss's own steps
+        rel += (8 + 8 + 16 + T / 4096 + 16) * U
         within(n64(r.prob_sums), want["prob_sums"], rel * want["prob_sums"] + T * TINY, "prob_sums")
         within(n64(r.loss), [want["loss"]], (rel + (E / 256 + 20) * U) * want["loss"] + TINY, "loss")
     return want
@@ -93,6 +93,43 @@ def test_route_difficult_logits(kind, bf16, renorm, T, E, k):
     mask = dev((torch.rand(T, generator=torch.Generator().manual_seed(4)) < 0.8).to(torch.uint8))
     for m in (None, mask):
         check_route(api.moe_route(z, k, token_mask=m, renorm=renorm, balance_coef=1.0), z, k, m, renorm, 1.0)
+
+
+@pytest.mark.parametrize("T,E,k,masked", [(9000, 257, 2, False), (33000, 12, 3, True), (40000, 100, 1, True),
+                                          (4096 * 3, 300, 9, True)])
+def test_route_of_many_tokens(T, E, k, masked):
+    """More chunks than one launch adds up, blocks of chunks that hold no row of an expert (or none at all), a ragged
+    last chunk.  The reference is vectorised here: sort by (expert, token)."""
+    z = logits_of(T, E, T, False)
+    z[:5000, 0] = -np.inf                      # expert 0 starts late
+    mask = torch.ones(T, dtype=torch.uint8)
+    if masked:
+        mask[:4200] = 0                        # the first block of chunks is padding
+        mask[T // 2:T // 2 + 77] = 0
+    r = api.moe_route(dev(z), k, token_mask=dev(mask) if masked else None, balance_coef=0.5)
+    live = mask.numpy() != 0
+    zz = np.where(live[:, None], z.numpy().astype(np.float64), -np.inf)
+    ids = np.argsort(-zz, axis=1, kind="stable")[:, :k]
+    ids[~live] = -1
+    assert np.array_equal(ints(r.expert_ids), ids)
+    flat = np.where(ids < 0, E, ids).ravel()
+    order = np.argsort(flat, kind="stable")
+    n = int((ids >= 0).sum())
+    rows = np.full(T * k, -1)
+    rows[order[:n]] = np.arange(n)
+    assert np.array_equal(ints(r.rows).ravel(), rows)
+    index = np.full(T * k, order[0] // k)
+    index[:n] = order[:n] // k
+    assert np.array_equal(ints(r.row_index), index)
+    count = np.bincount(flat, minlength=E + 1)[:E]
+    assert np.array_equal(ints(r.counts), np.append(count, live.sum()))
+    assert np.array_equal(ints(r.row_offsets), np.append(0, np.cumsum(count)))
+    assert np.array_equal(ints(r.sf_row_offsets), np.append(0, np.cumsum((count + 127) // 128 * 128)))
+    p = ref.softmax(zz, live).sum(0)
+    rel = (3 * ref.spread(z.numpy(), live) + 4 + -(-E // 32) + 5 + 3 + 8 + 8 + 8 + 8 + T / 4096 + 16) * U
+    within(n64(r.prob_sums), p, rel * p + T * TINY, "prob_sums")
+    loss = 0.5 * E * (count * p).sum() / k / live.sum() ** 2
+    within(n64(r.loss), [loss], (rel + (E / 32 + 20) * U) * loss, "loss")
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 8, 2), (130, 24, 3)])
