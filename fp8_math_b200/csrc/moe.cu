@@ -508,7 +508,7 @@ struct RouteOut {
 // there is, the CTA finishes the call (offsets, rows, loss).  L: k <= L by
 // sorted lists; 0: rounds for any k.
 template <typename In, int LPT, int Q, int L>
-__global__ void __launch_bounds__(512) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
+__global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                          int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
                                                          int renorm, int want_p, RouteOut out, int64_t nchunk,
                                                          uint8_t *__restrict__ hist, float *__restrict__ psum,
