@@ -21,11 +21,6 @@ BSQ_DEV float warp_sum(float v) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
 }
-BSQ_DEV float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-    return v;
-}
 BSQ_DEV uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&b);
@@ -730,24 +725,59 @@ __global__ void __launch_bounds__(256) route_block_kernel(const uint8_t *__restr
     }
 }
 
-// Sum over b0 <= b < b1 of p[b * stride], 16 loads in flight.
+// Sum of n values `stride` apart, 16 loads in flight; *part that of the first m.
 template <typename V>
-BSQ_DEV V column_sum(const V *p, int64_t stride, int64_t b0, int64_t b1) {
-    V s = 0;
-    for (int64_t b = b0; b < b1; b += 16) {
+BSQ_DEV V column_sum(const V *p, int64_t stride, int64_t n, int64_t m, V *part) {
+    V s = 0, first = 0;
+    for (int64_t b = 0; b < n; b += 16) {
         V v[16];
 #pragma unroll
-        for (int i = 0; i < 16; i++) v[i] = b + i < b1 ? __ldg(p + (b + i) * stride) : V(0);
+        for (int i = 0; i < 16; i++) v[i] = b + i < n ? __ldg(p + (b + i) * stride) : V(0);
 #pragma unroll
-        for (int i = 0; i < 16; i++) s += v[i];
+        for (int i = 0; i < 16; i++) {
+            s += v[i];
+            if (b + i < m) first += v[i];
+        }
     }
+    *part = first;
     return s;
+}
+
+// Exclusive scan of n[0..E), E <= 1024, into off[0..E] by a CTA of 256
+// threads, four neighbouring experts each.
+BSQ_DEV void cta_scan(const int32_t *n, int E, int32_t *off, int *wsum) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e0 = threadIdx.x * 4;
+    int v[4], s = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        v[i] = e0 + i < E ? n[e0 + i] : 0;
+        s += v[i];
+    }
+    int inc = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int at = inc - s;
+    for (int w = 0; w < warp; w++) at += wsum[w];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (e0 + i <= E) off[e0 + i] = at;
+        at += v[i];
+    }
+    if (E == 1024 && threadIdx.x == 255) off[E] = at;
+    __syncthreads();
 }
 
 // Pass 3.  Row of a slot = its expert's offset + the prefix of the blocks
 // before + the chunk's prefix in its block + the rank inside the chunk; the
 // rows past the last routed one repeat the first row's token.  A CTA takes
-// `span` chunks of one block; the last one also writes the offsets and the loss.
+// `span` chunks of one block; the last one also writes the offsets and the
+// loss.  (Laying the rows out by expert in shared memory, to write row_index
+// in runs, took 12 us more than the scattered writes at 131072x8 slots.)
 __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd, int E, int64_t nchunk, int span,
                                                           const uint8_t *__restrict__ hist,
                                                           const uint16_t *__restrict__ prefix,
@@ -756,51 +786,52 @@ __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd,
                                                           float coef) {
     grid_dependents_launch();
     grid_dependency_wait();
-    __shared__ int32_t base[kRouteMaxExperts + 1], all[kRouteMaxExperts + 1], off[kRouteMaxExperts + 1];
+    __shared__ int32_t base[kRouteMaxExperts], all[kRouteMaxExperts + 1], off[kRouteMaxExperts + 1];
     __shared__ float sums[kRouteMaxExperts];
-    __shared__ int first_chunk;
+    __shared__ int wsum[8], first_chunk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t blocks = gridDim.x, b = blockIdx.x;
-    const int64_t c0 = b * kBlock + blockIdx.y * span, c1 = min(min(c0 + span, (b + 1) * kBlock), nchunk);
-    for (int e = threadIdx.x; e <= E; e += 256) {
-        const int before = column_sum(count + e, E + 1, 0, b);
+    const int64_t c0 = min(b * kBlock + blockIdx.y * span, nchunk);
+    const int64_t c1 = max(c0, min(min(c0 + span, (b + 1) * kBlock), nchunk));
+    const uint32_t k = kd.d, i0 = (uint32_t)(min(c0 * kChunk, T) * k);  // slots i0 .. i0 + here, below 2^31
+    const int here = (int)((min(c1 * kChunk, T) - min(c0 * kChunk, T)) * k);
+    const uint16_t *at = prefix + c0 * E;
+    for (int e = threadIdx.x; e < E; e += 256) {
+        int before;
+        all[e] = column_sum(count + e, E + 1, blocks, b, &before);
         base[e] = before;
-        all[e] = before + column_sum(count + e, E + 1, b, blocks);
     }
     __syncthreads();
-    if (warp == 0) warp_scan<false>([&](int e) { return all[e]; }, E, off);
-    __syncthreads();
+    cta_scan(all, E, off, wsum);
     for (int e = threadIdx.x; e < E; e += 256) base[e] += off[e];
+    const int total = off[E];
     __syncthreads();
-    const uint32_t total = (uint32_t)off[E], k = kd.d;
-    const uint32_t i1 = (uint32_t)(min(c1 * kChunk, T) * k);  // below 2^31
     // four slots at a time, so that their loads overlap
-    for (uint32_t i0 = (uint32_t)(c0 * kChunk * k) + threadIdx.x; i0 < i1; i0 += 1024) {
+    for (int x0 = threadIdx.x; x0 < here; x0 += 1024) {
         int e[4], r[4];
+        uint32_t t[4];
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-            const uint32_t i = i0 + 256 * u;
-            e[u] = i < i1 ? __ldg(out.ids + i) : -1;
-            r[u] = i < i1 ? out.rows[i] : 0;
+            const int x = x0 + 256 * u;
+            e[u] = x < here ? __ldg(out.ids + i0 + x) : -1;
+            r[u] = x < here ? out.rows[i0 + x] : 0;
+            t[u] = divide(x, kd);
         }
 #pragma unroll
         for (int u = 0; u < 4; u++)
-            if (e[u] >= 0)
-                r[u] += base[e[u]] + (int)__ldg(prefix + (int64_t)(divide(i0 + 256 * u, kd) / kChunk) * E + e[u]);
+            if (e[u] >= 0) r[u] += base[e[u]] + __ldg(at + (t[u] / kChunk) * E + e[u]);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-            const uint32_t i = i0 + 256 * u;
-            if (e[u] >= 0) {
-                out.rows[i] = r[u];
-                out.row_index[r[u]] = (int32_t)divide(i, kd);
-            }
+            if (e[u] < 0) continue;
+            out.rows[i0 + x0 + 256 * u] = r[u];
+            out.row_index[r[u]] = (int)(c0 * kChunk) + (int)t[u];
         }
     }
-    if (c0 < c1 && i1 > total) {
+    if (here > 0 && (int64_t)i0 + here > total) {
         int token = 0;
         if (total > 0) {  // the first chunk that has the first row's expert, and its first token there
             int e0 = 0;
-            while (off[e0 + 1] == 0) e0++;
+            while (all[e0] == 0) e0++;
             int64_t b0 = 0;
             while (__ldg(count + b0 * (E + 1) + e0) == 0) b0++;
             if (threadIdx.x == 0) first_chunk = kBlock;
@@ -812,15 +843,18 @@ __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd,
             const int64_t c = b0 * kBlock + first_chunk;
             token = (int)(c * kChunk) + __ldg(hist + c * 2 * hist_row(E) + hist_row(E) + e0);
         }
-        for (uint32_t i = max((uint32_t)(c0 * kChunk * k), total) + threadIdx.x; i < i1; i += 256)
-            out.row_index[i] = token;
+        for (int x = threadIdx.x; x < here; x += 256)
+            if ((int64_t)i0 + x >= total) out.row_index[i0 + x] = token;
     }
     if (b < blocks - 1 || blockIdx.y < gridDim.y - 1) return;
     for (int e = threadIdx.x; e <= E; e += 256) {
+        int none;
+        if (e == E) all[E] = column_sum(count + E, E + 1, blocks, 0, &none);
         out.counts[e] = all[e];
         out.row_off[e] = off[e];
         if (psum_block && e < E) {
-            sums[e] = column_sum(psum_block + e, E, 0, blocks);
+            float part;
+            sums[e] = column_sum(psum_block + e, E, blocks, 0, &part);
             if (out.prob_sums) out.prob_sums[e] = sums[e];
         }
     }
@@ -1356,8 +1390,6 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-
-int launched() { return cudaGetLastError() == cudaSuccess ? 0 : 1; }
 
 // Whether quads of four logits are aligned in every row.
 template <typename In>
