@@ -30,6 +30,13 @@ BSQ_DEV float load_logit(const uint16_t *p) { return __uint_as_float((uint32_t)_
 BSQ_DEV void store_logit(float *p, float v) { *p = v; }
 BSQ_DEV void store_logit(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
 
+// a * b + c on an fp32 pair
+BSQ_DEV f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // 2^x (relative error 2^-22, results below 2^-126 are 0) and 1/x of a normal x (1 ulp).
 BSQ_DEV float ex2(float x) {
     float y;
@@ -313,11 +320,15 @@ BSQ_DEV void keep_best(float *v, const float *w) {
             if (!(i & h)) order2(v[i], v[i + h]);
 }
 template <int N>
-BSQ_DEV float entry(const float *v, int i) {
-    float r = v[0];
+BSQ_DEV float entry(const float *v, int i) {  // v[i % N]
+    float w[N];
 #pragma unroll
-    for (int j = 1; j < N; j++) r = i == j ? v[j] : r;
-    return r;
+    for (int j = 0; j < N; j++) w[j] = v[j];
+#pragma unroll
+    for (int h = 1; h < N; h <<= 1)
+#pragma unroll
+        for (int j = 0; j < N; j += 2 * h) w[j] = i & h ? w[j + h] : w[j];
+    return w[0];
 }
 template <typename In>
 BSQ_DEV uint32_t expert_bits(int E) {
@@ -494,8 +505,8 @@ struct RouteOut {
     float *prob_sums, *loss;
 };
 
-// Pass 1.  A CTA takes kChunk consecutive tokens, LPT lanes a token.  The
-// softmax sum runs over the same registers as the choice.  The chosen experts
+// Pass 1.  A CTA takes chunks of kChunk consecutive tokens in turn, LPT lanes a
+// token; the sums of probabilities stay in its registers.  The softmax sum runs over the same registers as the choice.  The chosen experts
 // go into one 64-bit mask of tokens per expert, whose population count is the
 // chunk's count and whose bits below a token are that token's rank in the
 // chunk: the order "by expert, then token" needs no sort.  Row E of the counts
@@ -520,10 +531,6 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
     uint16_t *sel = reinterpret_cast<uint16_t *>(off + (nchunk == 1 ? E + 1 : 0));     // [kChunk][k]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPT;
     constexpr int kGroups = 32 / LPT;
-    for (int i = threadIdx.x; i < 2 * (E + 1); i += blockDim.x) words[i] = 0;
-    __syncthreads();
-    const int64_t t0 = (int64_t)blockIdx.x * kChunk;
-    const int here = (int)min((int64_t)kChunk, T - t0);
     const bool single = nchunk == 1;
     auto pick = [&](int tl, int j, int e, float x) {
         sel[tl * k + j] = (uint16_t)e;
@@ -531,117 +538,135 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
         if (e >= 0) atomicOr(&words[2 * e + (tl >> 5)], 1u << (tl & 31));
         if (j == 0 && e >= 0) atomicOr(&words[2 * E + (tl >> 5)], 1u << (tl & 31));
     };
-    float acc[Q][4];
+    f32x2 acc[Q][2];
 #pragma unroll
-    for (int q = 0; q < Q; q++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) acc[q][i] = 0.0f;
-    for (int w0 = warp * kGroups; w0 < here; w0 += nwarps * kGroups) {
-        const int tl = w0 + lane / LPT;
-        const bool in = tl < here;
-        const bool live = in && (!mask || __ldg(mask + t0 + tl) != 0);
-        Row<In, LPT, Q> row;
-        row.load(logits + (t0 + tl) * ldl, E, sub, vec, live);
-        float top = 0.0f, chosen = 0.0f;
-        bool done = false;
-        if (L > 0) {
-            int e;
-            float z;
-            done = choose<L == 0 ? 4 : L>(row, logits + (t0 + tl) * ldl, sub, E, vec, k, e, z);
-            if (done) {  // the same for the whole warp
-                top = __shfl_sync(kFull, e >= 0 ? z : 0.0f, lane & ~(LPT - 1));
-                const float x = e >= 0 ? ex2((z - top) * kLog2e) : 0.0f;
-                chosen = group_sum<LPT>(x);
-                if (in && sub < k) pick(tl, sub, e, x);
-            }
-        }
-        if (!done) {
-            Candidates<In, LPT, Q> c;
-            c.template fill<false>(row, sub, 0.0f);
-            for (int j0 = 0; j0 < k; j0 += LPT) {
-                int my_e = -1;
-                float my_x = 0.0f;
-                for (int j = j0; j < min(k, j0 + LPT); j++) {
-                    int e;
-                    const float z = c.pop(row, sub, e);
-                    const bool ok = z > -INFINITY;
-                    if (j == 0 && ok) top = z;
-                    const float x = ok ? ex2((z - top) * kLog2e) : 0.0f;
-                    chosen += x;
-                    if (ok && sub == j - j0) {
-                        my_e = e;
-                        my_x = x;
-                    }
+    for (int q = 0; q < Q; q++) acc[q][0] = acc[q][1] = f2_pack(0.0f, 0.0f);
+    for (int64_t chunk = blockIdx.x; chunk < nchunk; chunk += gridDim.x) {
+        for (int i = threadIdx.x; i < 2 * (E + 1); i += blockDim.x) words[i] = 0;
+        __syncthreads();
+        const int64_t t0 = chunk * kChunk;
+        const int here = (int)min((int64_t)kChunk, T - t0);
+        for (int w0 = warp * kGroups; w0 < here; w0 += nwarps * kGroups) {
+            const int tl = w0 + lane / LPT;
+            const bool in = tl < here;
+            const bool live = in && (!mask || __ldg(mask + t0 + tl) != 0);
+            Row<In, LPT, Q> row;
+            row.load(logits + (t0 + tl) * ldl, E, sub, vec, live);
+            float top = 0.0f, chosen = 0.0f;
+            bool done = false;
+            if (L > 0) {
+                int e;
+                float z;
+                done = choose<L == 0 ? 4 : L>(row, logits + (t0 + tl) * ldl, sub, E, vec, k, e, z);
+                if (done) {  // the same for the whole warp
+                    top = __shfl_sync(kFull, e >= 0 ? z : 0.0f, lane & ~(LPT - 1));
+                    const float x = e >= 0 ? ex2((z - top) * kLog2e) : 0.0f;
+                    chosen = group_sum<LPT>(x);
+                    if (in && sub < k) pick(tl, sub, e, x);
                 }
-                if (in && j0 + sub < k) pick(tl, j0 + sub, my_e, my_x);  // a lane per slot
             }
-        }
-        if (want_p || !renorm) {
-            const f32x2 top2 = f2_pack(top, top);
-            float s = 0.0f;
-            float p[Q][4];
-#pragma unroll
-            for (int q = 0; q < Q; q++) {
-                row.get(q, p[q]);
-                exp_below4(p[q], top2);
-                s += (p[q][0] + p[q][1]) + (p[q][2] + p[q][3]);
+            if (!done) {
+                Candidates<In, LPT, Q> c;
+                c.template fill<false>(row, sub, 0.0f);
+                for (int j0 = 0; j0 < k; j0 += LPT) {
+                    int my_e = -1;
+                    float my_x = 0.0f;
+                    for (int j = j0; j < min(k, j0 + LPT); j++) {
+                        int e;
+                        const float z = c.pop(row, sub, e);
+                        const bool ok = z > -INFINITY;
+                        if (j == 0 && ok) top = z;
+                        const float x = ok ? ex2((z - top) * kLog2e) : 0.0f;
+                        chosen += x;
+                        if (ok && sub == j - j0) {
+                            my_e = e;
+                            my_x = x;
+                        }
+                    }
+                    if (in && j0 + sub < k) pick(tl, j0 + sub, my_e, my_x);  // a lane per slot
+                }
             }
-            s = group_sum<LPT>(s);
-            const float r = s > 0.0f ? rcp(s) : 0.0f;
-            if (want_p)
+            if (want_p || !renorm) {
+                const f32x2 top2 = f2_pack(top, top);
+                f32x2 s2 = f2_pack(0.0f, 0.0f), p[Q][2];
 #pragma unroll
-                for (int q = 0; q < Q; q++)
+                for (int q = 0; q < Q; q++) {
+                    float x[4];
+                    row.get(q, x);
+                    exp_below4(x, top2);
+                    p[q][0] = f2_pack(x[0], x[1]);
+                    p[q][1] = f2_pack(x[2], x[3]);
+                    s2 = f2_add(s2, f2_add(p[q][0], p[q][1]));
+                }
+                float s, s_odd;
+                f2_unpack(s2, s, s_odd);
+                s = group_sum<LPT>(s + s_odd);
+                const float r = s > 0.0f ? rcp(s) : 0.0f;
+                const f32x2 r2 = f2_pack(r, r);
+                if (want_p)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) acc[q][i] = fmaf(p[q][i], r, acc[q][i]);
-            if (!renorm) chosen = s;
+                    for (int q = 0; q < Q; q++) {
+                        acc[q][0] = f2_fma(p[q][0], r2, acc[q][0]);
+                        acc[q][1] = f2_fma(p[q][1], r2, acc[q][1]);
+                    }
+                if (!renorm) chosen = s;
+            }
+            if (in && sub == 0) inv[tl] = chosen > 0.0f ? rcp(chosen) : 0.0f;
         }
-        if (in && sub == 0) inv[tl] = chosen > 0.0f ? rcp(chosen) : 0.0f;
+        __syncthreads();
+        if (single) {
+            if (warp == 0) warp_scan<false>([&](int e) { return __popcll(smem[e]); }, E, off);
+            __syncthreads();
+        }
+        for (int i = threadIdx.x; i < here * k; i += blockDim.x) {
+            const int tl = (int)divide((uint32_t)i, kd);
+            const int e = (int16_t)sel[i];
+            int row = e < 0 ? -1 : __popcll(smem[e] & ((1ull << tl) - 1ull));
+            if (single && e >= 0) {
+                row += off[e];
+                out.row_index[row] = tl;
+            }
+            out.ids[t0 * k + i] = e;
+            out.weights[t0 * k + i] = sel_x[i] * inv[tl];
+            out.rows[t0 * k + i] = row;
+        }
+        if (!single) {
+            // a row of counts and a row of first tokens per chunk
+            uint8_t *to = hist + chunk * 2 * hist_row(E);
+            for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+                const unsigned long long m = smem[e];
+                to[e] = (uint8_t)__popcll(m);
+                to[hist_row(E) + e] = (uint8_t)(m ? __ffsll(m) - 1 : 0);
+            }
+            __syncthreads();
+        }
     }
     if (want_p) {
 #pragma unroll
-        for (int q = 0; q < Q; q++)
+        for (int q = 0; q < Q; q++) {
+            float a4[4];
+            f2_unpack(acc[q][0], a4[0], a4[1]);
+            f2_unpack(acc[q][1], a4[2], a4[3]);
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                float v = acc[q][i];
+                float v = a4[i];
 #pragma unroll
                 for (int o = LPT; o < 32; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
                 const int e = 4 * (q * LPT + sub) + i;
                 if (lane < LPT && e < E) red[warp * E + e] = v;
             }
-    }
-    __syncthreads();
-    if (single) {
-        if (warp == 0) warp_scan<false>([&](int e) { return __popcll(smem[e]); }, E, off);
+        }
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < here * k; i += blockDim.x) {
-        const int tl = (int)divide((uint32_t)i, kd);
-        const int e = (int16_t)sel[i];
-        int row = e < 0 ? -1 : __popcll(smem[e] & ((1ull << tl) - 1ull));
-        if (single && e >= 0) {
-            row += off[e];
-            out.row_index[row] = tl;
-        }
-        out.ids[t0 * k + i] = e;
-        out.weights[t0 * k + i] = sel_x[i] * inv[tl];
-        out.rows[t0 * k + i] = row;
-    }
     if (!single) {
-        for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-            const unsigned long long m = smem[e];
-            const uint32_t n = (uint32_t)__popcll(m), first = m ? (uint32_t)(__ffsll(m) - 1) : 0u;
-            // a row of counts and a row of first tokens per chunk
-            uint8_t *to = hist + (int64_t)blockIdx.x * 2 * hist_row(E);
-            to[e] = (uint8_t)n;
-            to[hist_row(E) + e] = (uint8_t)first;
-            if (want_p && e < E) {
+        if (want_p)
+            for (int e = threadIdx.x; e < E; e += blockDim.x) {
                 float v = 0.0f;
                 for (int w = 0; w < nwarps; w++) v += red[w * E + e];
                 psum[(int64_t)blockIdx.x * E + e] = v;
             }
-        }
     } else {
-        const int total = off[E], tokens = __popcll(smem[E]);
+        const int here = (int)T, total = off[E], tokens = __popcll(smem[E]);
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
             if (off[e] == 0 && off[e + 1] > 0)  // the expert of the first row, and its first token
                 for (int i = total; i < here * k; i++) out.row_index[i] = __ffsll(smem[e]) - 1;
@@ -676,12 +701,13 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
 // Pass 2, for many chunks.  A CTA takes kBlock consecutive chunks and 32 experts
 // (row E, the tokens, among them), a lane one expert and a warp a run of the
 // chunks, all loads in flight at once: the exclusive prefix of every chunk
-// inside the block, and the block's counts and sums of probabilities.
+// inside the block, and the block's counts.  The first pass's rows of sums of
+// probabilities are added up along the way, spread over the blocks.
 constexpr int kBlock = 64, kRun = kBlock / 8;
 
 __global__ void __launch_bounds__(256) route_block_kernel(const uint8_t *__restrict__ hist,
-                                                          const float *__restrict__ psum, int64_t nchunk, int E,
-                                                          uint16_t *__restrict__ prefix, int32_t *__restrict__ count,
+                                                          const float *__restrict__ psum, int64_t rows, int64_t nchunk,
+                                                          int E, uint16_t *__restrict__ prefix, int32_t *__restrict__ count,
                                                           float *__restrict__ psum_block) {
     grid_dependents_launch();
     grid_dependency_wait();
@@ -691,17 +717,15 @@ __global__ void __launch_bounds__(256) route_block_kernel(const uint8_t *__restr
     const int e = blockIdx.y * 32 + lane, row = hist_row(E);
     const int64_t c = (int64_t)blockIdx.x * kBlock + warp * kRun;
     int v[kRun], n = 0;
-    float f[kRun], p = 0.0f;
+    float p = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kRun; i++) {
-        v[i] = c + i < nchunk && e <= E ? __ldg(hist + (c + i) * 2 * row + e) : 0;
-        f[i] = c + i < nchunk && e < E && psum ? __ldg(psum + (c + i) * E + e) : 0.0f;
-    }
+    for (int i = 0; i < kRun; i++) v[i] = c + i < nchunk && e <= E ? __ldg(hist + (c + i) * 2 * row + e) : 0;
+    if (psum && e < E)
+#pragma unroll 4
+        for (int64_t i = blockIdx.x + (int64_t)warp * gridDim.x; i < rows; i += 8 * (int64_t)gridDim.x)
+            p += __ldg(psum + i * E + e);
 #pragma unroll
-    for (int i = 0; i < kRun; i++) {
-        n += v[i];
-        p += f[i];
-    }
+    for (int i = 0; i < kRun; i++) n += v[i];
     run[warp][lane] = n;
     fsum[warp][lane] = p;
     __syncthreads();
@@ -878,7 +902,7 @@ constexpr int kSmallHist = 48 * 1024, kSmallChunks = 512;
 
 __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDiv kd, int E, int nchunk,
                                                                UnitDiv wd, const uint8_t *__restrict__ hist,
-                                                               const float *__restrict__ psum, RouteOut out,
+                                                               const float *__restrict__ psum, int64_t rows, RouteOut out,
                                                                float coef) {
     grid_dependents_launch();
     grid_dependency_wait();
@@ -906,12 +930,12 @@ __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDi
         const int parts = 256 / E, e = threadIdx.x % E, g = threadIdx.x / E;
         float p = 0.0f;
         if (g < parts)
-            for (int c0 = g; c0 < nchunk; c0 += 16 * parts) {
+            for (int c0 = g; c0 < rows; c0 += 16 * parts) {
                 float v[16];
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     const int c = c0 + i * parts;
-                    v[i] = c < nchunk ? __ldg(psum + c * E + e) : 0.0f;
+                    v[i] = c < rows ? __ldg(psum + c * E + e) : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < 16; i++) p += v[i];
@@ -1418,6 +1442,15 @@ bool small_hist(int64_t nchunk, int E) {
     return E <= 256 && nchunk <= kSmallChunks && nchunk * hist_row(E) <= kSmallHist;
 }
 
+// First pass: 16 warps take a chunk in half as many turns, while all chunks fit
+// on the SMs at once; else 8 warps.  Many experts: two chunks a CTA, so that the
+// sums of probabilities leave the registers half as often (more leaves the last
+// CTAs alone: 131072x256 takes 67 us with as many CTAs as fit, 64 with this).
+int topk_threads(int64_t nchunk, int num_sms) { return nchunk <= 2 * num_sms ? 512 : 256; }
+int64_t topk_grid(int64_t nchunk, int64_t E, int num_sms) {
+    return E > 128 && topk_threads(nchunk, num_sms) == 256 ? (nchunk + 1) / 2 : nchunk;
+}
+
 // Shared memory of the first pass; at most 89,608 bytes (1024 experts, 32 slots, 16 warps).
 constexpr int kRouteSmem = 96 * 1024;
 
@@ -1436,8 +1469,7 @@ struct TopkLaunch {
     template <class K>
     int run(K kern) const {
         const int E = (int)a.E, k = a.topk;
-        // 16 warps take the chunk in half as many turns: while all chunks fit on the SMs at once
-        const int threads = w.nchunk <= 2 * num_sms ? 512 : 256;
+        const int threads = topk_threads(w.nchunk, num_sms);
         const size_t smem = 8 * (size_t)(E + 1) + 4 * kChunk * (size_t)(k + 1) +
                             (want_p ? threads / 32 * 4 * (size_t)E : 0) + (w.nchunk == 1 ? 4 * (size_t)(E + 1) : 0) +
                             2 * kChunk * (size_t)k;
@@ -1445,7 +1477,7 @@ struct TopkLaunch {
         const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
                            a.loss};
         return launch_dependent(
-                   kern, dim3((unsigned)w.nchunk), dim3(threads), smem, s, static_cast<const In *>(a.logits), a.T, E,
+                   kern, dim3((unsigned)topk_grid(w.nchunk, E, num_sms)), dim3(threads), smem, s, static_cast<const In *>(a.logits), a.T, E,
                    a.ldl, (int)quads<In>(a.logits, E, a.ldl), a.mask, unit_div((uint32_t)k), (int)a.renorm, want_p, out,
                    w.nchunk, a.ws + w.hist, reinterpret_cast<float *>(a.ws + w.psum), a.coef) != cudaSuccess;
     }
@@ -1490,20 +1522,21 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
                : by_experts(a.E, TopkLaunch<float>{a, w, want_p, num_sms, s}))
         return 1;
     if (w.nchunk == 1) return 0;
+    const int64_t rows = topk_grid(w.nchunk, a.E, num_sms);  // of sums of probabilities
     const int E = (int)a.E;
     float *psum = want_p ? reinterpret_cast<float *>(a.ws + w.psum) : nullptr;
     const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums, a.loss};
     if (small_hist(w.nchunk, E))
         return launch_dependent(route_scan_place_kernel, dim3((unsigned)w.nchunk + 1), dim3(256), 0, s, a.T,
                                 unit_div((uint32_t)a.topk), E, (int)w.nchunk,
-                                unit_div((uint32_t)hist_row(E) / 4), (const uint8_t *)(a.ws + w.hist), (const float *)psum, out,
+                                unit_div((uint32_t)hist_row(E) / 4), (const uint8_t *)(a.ws + w.hist), (const float *)psum, rows, out,
                                 a.coef) != cudaSuccess;
     const int64_t blocks = (w.nchunk + kBlock - 1) / kBlock;
     uint16_t *prefix = reinterpret_cast<uint16_t *>(a.ws + w.prefix);
     int32_t *count = reinterpret_cast<int32_t *>(a.ws + w.count);
     float *psum_block = want_p ? reinterpret_cast<float *>(a.ws + w.psum_block) : nullptr;
     if (launch_dependent(route_block_kernel, dim3((unsigned)blocks, E / 32 + 1), dim3(256), 0, s,
-                         (const uint8_t *)(a.ws + w.hist), (const float *)psum, w.nchunk, E, prefix, count,
+                         (const uint8_t *)(a.ws + w.hist), (const float *)psum, rows, w.nchunk, E, prefix, count,
                          psum_block) != cudaSuccess)
         return 1;
     // about three CTAs per SM: each adds up all blocks' counts
