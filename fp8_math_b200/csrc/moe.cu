@@ -112,6 +112,10 @@ struct Row<uint16_t, LPT, Q> {
             }
         }
     }
+    BSQ_DEV void clear() {
+#pragma unroll
+        for (int q = 0; q < Q; q++) w[q] = make_uint2(0xFF80FF80u, 0xFF80FF80u);
+    }
     BSQ_DEV float quad_max(int q) const {
         uint32_t m;
         asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w[q].x), "r"(w[q].y));
@@ -143,6 +147,10 @@ struct Row<float, LPT, Q> {
                 if (e + 3 < E) w[q].w = __ldg(row + e + 3);
             }
         }
+    }
+    BSQ_DEV void clear() {
+#pragma unroll
+        for (int q = 0; q < Q; q++) w[q] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
     BSQ_DEV float quad_max(int q) const {
         return fmaxf(fmaxf(w[q].x, w[q].y), fmaxf(w[q].z, w[q].w));
@@ -1060,30 +1068,45 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ l
     __syncthreads();
     const int64_t stride = (int64_t)gridDim.x * 8 * kGroups;
     // a warp's tokens start together: the shuffles want whole warps
-    for (int64_t w0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kGroups; w0 < T; w0 += stride) {
-        const int64_t t = w0 + lane / LPT;
+    for (int64_t t0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * kGroups; t0 < T; t0 += stride) {
+        const int64_t t = t0 + lane / LPT;
         const bool in = t < T;
-        float dot = 0.0f;
-        bool live = false;
-        for (int j = sub; j < k; j += LPT) {
-            const int e = in ? __ldg(ids + t * k + j) : -1;
+        Row<In, LPT, Q> row;
+        if (NEED_P) row.load(logits + t * ldl, E, sub, vec, in);  // in flight with the choice
+        // slot sub in registers, slots sub + LPT, ... (k > LPT) by the loops
+        const uint32_t slot = (uint32_t)t * (uint32_t)k + sub;  // T k < 2^31
+        int e0 = -1;
+        float w0 = 0.0f, a0 = 0.0f;
+        if (in && sub < k) {
+            e0 = __ldg(ids + slot);
+            if (dweights) {
+                w0 = __ldg(weights + slot);
+                a0 = __ldg(dweights + slot);
+            }
+        }
+        const bool has = (unsigned)e0 < (unsigned)E;
+        bool live = has;
+        float dot = has ? w0 * a0 : 0.0f;
+        for (int j = LPT; sub + j < k; j += LPT) {
+            const int e = in ? __ldg(ids + slot + j) : -1;
             if ((unsigned)e >= (unsigned)E) continue;
             live = true;
-            if (dweights) dot = fmaf(__ldg(weights + t * k + j), __ldg(dweights + t * k + j), dot);
+            if (dweights) dot = fmaf(__ldg(weights + slot + j), __ldg(dweights + slot + j), dot);
         }
         const unsigned any = __ballot_sync(kFull, live);
         const unsigned mine = LPT == 32 ? kFull : ((1u << (LPT & 31)) - 1u) << (lane & ~(LPT - 1));
-        live = (any & mine) != 0;  // a masked token's logits are not read
-        Row<In, LPT, Q> row;
-        if (NEED_P) row.load(logits + t * ldl, E, sub, vec, live);
+        live = (any & mine) != 0;
+        if (NEED_P && !live) row.clear();  // a masked token's logits may be anything
         dot = group_sum<LPT>(dot);  // sum over the chosen of q a: both kinds of q have q_ej = w_j
         // the chosen experts' own term: w_j (a_j - dot), or w_j a_j where dot goes over all experts
-        if (dweights)
-            for (int j = sub; j < k; j += LPT) {
-                const int e = in ? __ldg(ids + t * k + j) : -1;
-                if ((unsigned)e >= (unsigned)E) continue;
-                own_row[e] = __ldg(weights + t * k + j) * (__ldg(dweights + t * k + j) - (renorm ? dot : 0.0f));
+        const float all = renorm ? dot : 0.0f;
+        if (dweights) {
+            if (has) own_row[e0] = w0 * (a0 - all);
+            for (int j = LPT; sub + j < k; j += LPT) {
+                const int e = in ? __ldg(ids + slot + j) : -1;
+                if ((unsigned)e < (unsigned)E) own_row[e] = __ldg(weights + slot + j) * (__ldg(dweights + slot + j) - all);
             }
+        }
         float d[Q][4], sub_all = 0.0f, inv = 0.0f;
         if (NEED_P) {
             float top = -INFINITY;
@@ -1095,29 +1118,33 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ l
             top = group_max<LPT>(top);
             if (!(top > -INFINITY)) top = 0.0f;
             const f32x2 top2 = f2_pack(top, top);
-            float s = 0.0f, pb = 0.0f;
+            f32x2 s2 = f2_pack(0.0f, 0.0f), pb2 = s2;
 #pragma unroll
             for (int q = 0; q < Q; q++) {
                 exp_below4(d[q], top2);
                 const float4 b = *reinterpret_cast<const float4 *>(bias + 4 * (q * LPT + sub));
-                s += (d[q][0] + d[q][1]) + (d[q][2] + d[q][3]);
-                pb += (d[q][0] * b.x + d[q][1] * b.y) + (d[q][2] * b.z + d[q][3] * b.w);
+                const f32x2 p0 = f2_pack(d[q][0], d[q][1]), p1 = f2_pack(d[q][2], d[q][3]);
+                s2 = f2_add(s2, f2_add(p0, p1));
+                pb2 = f2_fma(p0, f2_pack(b.x, b.y), f2_fma(p1, f2_pack(b.z, b.w), pb2));
             }
-            s = group_sum<LPT>(s);
+            float s, pb, odd;
+            f2_unpack(s2, s, odd);
+            s = group_sum<LPT>(s + odd);
             inv = s > 0.0f ? rcp(s) : 0.0f;
-            sub_all = group_sum<LPT>(pb) * inv + (renorm ? 0.0f : dot);
+            f2_unpack(pb2, pb, odd);
+            sub_all = group_sum<LPT>(pb + odd) * inv + (renorm ? 0.0f : dot);
         }
         __syncwarp();
+        const f32x2 inv2 = f2_pack(inv, inv), sub2 = f2_pack(sub_all, sub_all);
 #pragma unroll
         for (int q = 0; q < Q; q++) {
             const int e = 4 * (q * LPT + sub);
             const float4 o = *reinterpret_cast<const float4 *>(own_row + e);
             if (NEED_P) {
                 const float4 b = *reinterpret_cast<const float4 *>(bias + e);
-                d[q][0] = fmaf(d[q][0] * inv, b.x - sub_all, o.x);
-                d[q][1] = fmaf(d[q][1] * inv, b.y - sub_all, o.y);
-                d[q][2] = fmaf(d[q][2] * inv, b.z - sub_all, o.z);
-                d[q][3] = fmaf(d[q][3] * inv, b.w - sub_all, o.w);
+                const f32x2 p0 = f2_mul(f2_pack(d[q][0], d[q][1]), inv2), p1 = f2_mul(f2_pack(d[q][2], d[q][3]), inv2);
+                f2_unpack(f2_fma(p0, f2_sub(f2_pack(b.x, b.y), sub2), f2_pack(o.x, o.y)), d[q][0], d[q][1]);
+                f2_unpack(f2_fma(p1, f2_sub(f2_pack(b.z, b.w), sub2), f2_pack(o.z, o.w)), d[q][2], d[q][3]);
             } else {
                 d[q][0] = o.x;
                 d[q][1] = o.y;
@@ -1135,11 +1162,13 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ l
             }
         }
         __syncwarp();
-        if (dweights)
-            for (int j = sub; j < k; j += LPT) {
-                const int e = in ? __ldg(ids + t * k + j) : -1;
+        if (dweights) {
+            if (has) own_row[e0] = 0.0f;
+            for (int j = LPT; sub + j < k; j += LPT) {
+                const int e = in ? __ldg(ids + slot + j) : -1;
                 if ((unsigned)e < (unsigned)E) own_row[e] = 0.0f;
             }
+        }
         __syncwarp();
     }
 }
