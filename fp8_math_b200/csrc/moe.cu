@@ -1032,6 +1032,14 @@ BSQ_DEV void store4(uint16_t *p, const float d[4]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]));
 }
 
+// CTAs per SM, and the grid is no larger: five at 48 registers where a lane's
+// logits leave that many free, six where the softmax is not needed (shared
+// memory).  131072x256 takes 50 us with eight CTAs per SM in turns, 35 with three.
+template <int Q, bool NEED_P>
+constexpr int bwd_ctas() {
+    return !NEED_P ? 6 : Q <= 5 ? 5 : 3;
+}
+
 // LPT lanes per token.  With q the weights' distribution (the softmax over all
 // experts, or over the chosen ones) and a_e = dL/dweight of expert e (zero
 // where it was not chosen): dz_e = q_e (a_e - sum q a).  The balance loss adds
@@ -1040,7 +1048,7 @@ BSQ_DEV void store4(uint16_t *p, const float d[4]) {
 // lanes that hold those experts through a row of shared memory per token,
 // which is zero between tokens.
 template <typename In, int LPT, int Q, bool NEED_P>
-__global__ void __launch_bounds__(256) route_bwd_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
+__global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                         int vec, int k, int renorm, const int32_t *__restrict__ ids,
                                                         const float *__restrict__ weights,
                                                         const float *__restrict__ dweights,
@@ -1520,7 +1528,7 @@ struct BwdLaunch {
     template <int LPT, int Q>
     int operator()() const {
         constexpr int per_cta = 8 * (32 / LPT);
-        const unsigned grid = (unsigned)std::min<int64_t>((a.T + per_cta - 1) / per_cta, (int64_t)num_sms * 8);
+        const unsigned grid = (unsigned)std::min<int64_t>((a.T + per_cta - 1) / per_cta, (int64_t)num_sms * bwd_ctas<Q, NEED_P>());
         const bool vec = quads<In>(a.logits, a.E, a.ldl) && quads<In>(a.dlogits, a.E, a.ldd);
         return launch_dependent(route_bwd_kernel<In, LPT, Q, NEED_P>, dim3(grid), dim3(256), 0, s,
                                 static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, (int)vec, a.topk,
