@@ -1209,33 +1209,35 @@ __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict
                                                                pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
 }
 
-// 16 values of an MXFP8 row from their codes and the block's scale code.
-BSQ_DEV void mx_decode16(uint4 q, uint32_t sb, f32x2 v[8]) {
-    const float scale = exp2i((int)sb - 127);
-    const f32x2 s2 = f2_pack(scale, scale);
+// 2^(code - 127) of an E8M0 code (0: 2^-127, a subnormal).
+BSQ_DEV float e8m0_value(uint32_t code) { return __uint_as_float(code ? code << 23 : 0x00400000u); }
+
+// 16 E4M3 codes as fp32 pairs, without their block's scale.
+BSQ_DEV void e4m3x16(uint4 q, f32x2 v[8]) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         float a, b, c, d;
         e4m3x2_to_f32(w[i] & 0xFFFFu, a, b);
         e4m3x2_to_f32(w[i] >> 16, c, d);
-        v[2 * i] = f2_mul(f2_pack(a, b), s2);
-        v[2 * i + 1] = f2_mul(f2_pack(c, d), s2);
+        v[2 * i] = f2_pack(a, b);
+        v[2 * i + 1] = f2_pack(c, d);
     }
 }
 
 // Eight columns: the dot product's terms, and w times dout in bf16.
-BSQ_DEV void bwd8(uint4 dq, const float v[8], float w, float &dot, uint4 *to) {
+BSQ_DEV void bwd8(uint4 dq, const f32x2 v[4], f32x2 w2, f32x2 &dot2, uint16_t *to) {
     const uint32_t d[4] = {dq.x, dq.y, dq.z, dq.w};
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; i++) {
-        const float d0 = bf16_lo(d[i]), d1 = bf16_hi(d[i]);
-        dot = fmaf(d0, v[2 * i], dot);
-        dot = fmaf(d1, v[2 * i + 1], dot);
-        o[i] = pack_bf16(w * d0, w * d1);
+        const f32x2 d2 = f2_pack(bf16_lo(d[i]), bf16_hi(d[i]));
+        dot2 = f2_fma(d2, v[i], dot2);
+        float a, b;
+        f2_unpack(f2_mul(d2, w2), a, b);
+        o[i] = pack_bf16(a, b);
     }
-    *to = make_uint4(o[0], o[1], o[2], o[3]);
+    *reinterpret_cast<uint4 *>(to) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // dy[rows_tj] = w_tj dout_t and dw_tj = <dout_t, y[rows_tj]>: one warp per
@@ -1257,40 +1259,44 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__rest
     if (slot >= slots) return;
     const int lane = threadIdx.x & 31;
     const int64_t r = __ldg(rows + slot);
-    float dot = 0.0f;
+    const f32x2 zero2 = f2_pack(0.0f, 0.0f);
+    f32x2 dot2 = zero2;
     if (r >= 0 && r < R) {
         const float w = __ldg(weights + slot);
+        const f32x2 w2 = f2_pack(w, w);
         const uint16_t *drow = dout + (int64_t)divide(slot, k) * ldo;
         uint16_t *to = dy + r * lddy;
+        const int cols = (int)H;  // at most 2^25
         if (MX) {
             const uint8_t *crow = codes + r * H;
             const uint8_t *srow = sf + sf_offset(r, 0, H >> 5);
 #pragma unroll 2
-            for (int64_t c = lane * 16; c < H; c += 512) {
+            for (int c = lane * 16; c < cols; c += 512) {
                 const uint4 q = __ldg(reinterpret_cast<const uint4 *>(crow + c));
                 const uint4 d0 = __ldg(reinterpret_cast<const uint4 *>(drow + c));
                 const uint4 d1 = __ldg(reinterpret_cast<const uint4 *>(drow + c + 8));
-                const uint32_t sb = __ldg(srow + ((c >> 7) << 9) + ((c >> 5) & 3));  // an atom per four blocks
-                f32x2 v2[8];
-                mx_decode16(q, sb, v2);
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 8; i++) f2_unpack(v2[i], v[2 * i], v[2 * i + 1]);
-                bwd8(d0, v, w, dot, reinterpret_cast<uint4 *>(to + c));
-                bwd8(d1, v + 8, w, dot, reinterpret_cast<uint4 *>(to + c + 8));
+                const float scale = e8m0_value(__ldg(srow + ((c >> 7) << 9) + ((c >> 5) & 3)));  // atoms of 4 blocks
+                f32x2 v[8], part2 = zero2;
+                e4m3x16(q, v);
+                bwd8(d0, v, w2, part2, to + c);
+                bwd8(d1, v + 4, w2, part2, to + c + 8);
+                dot2 = f2_fma(part2, f2_pack(scale, scale), dot2);
             }
         } else {
             const uint16_t *yrow = y + r * ldy;
 #pragma unroll 4
-            for (int64_t c = lane * 8; c < H; c += 256) {
-                float v[8];
+            for (int c = lane * 8; c < cols; c += 256) {
                 const uint4 d = __ldg(reinterpret_cast<const uint4 *>(drow + c));
-                load8_bf16(yrow + c, v);
-                bwd8(d, v, w, dot, reinterpret_cast<uint4 *>(to + c));
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(yrow + c));
+                const f32x2 v[4] = {f2_pack(bf16_lo(q.x), bf16_hi(q.x)), f2_pack(bf16_lo(q.y), bf16_hi(q.y)),
+                                    f2_pack(bf16_lo(q.z), bf16_hi(q.z)), f2_pack(bf16_lo(q.w), bf16_hi(q.w))};
+                bwd8(d, v, w2, dot2, to + c);
             }
         }
     }
-    dot = warp_sum(dot);
+    float dot, odd;
+    f2_unpack(dot2, dot, odd);
+    dot = warp_sum(dot + odd);
     if (lane == 0) dweights[slot] = dot;
 }
 
@@ -1424,8 +1430,15 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__
         load16(dh + r * lddh + c, d);
         const uint4 qg = __ldg(reinterpret_cast<const uint4 *>(row)), qv = __ldg(reinterpret_cast<const uint4 *>(row + F));
         const uint32_t sg = __ldg(sf + sf_offset(r, c >> 5, F >> 4)), sv = __ldg(sf + sf_offset(r, (c + F) >> 5, F >> 4));
-        mx_decode16(qg, sg, g);
-        mx_decode16(qv, sv, v);
+        e4m3x16(qg, g);
+        e4m3x16(qv, v);
+        const float fg = e8m0_value(sg), fv = e8m0_value(sv);
+        const f32x2 fg2 = f2_pack(fg, fg), fv2 = f2_pack(fv, fv);
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+            g[q] = f2_mul(g[q], fg2);
+            v[q] = f2_mul(v[q], fv2);
+        }
 #pragma unroll
         for (int q = 0; q < 8; q++) {
             float gg[2], vv[2], dx[2], dy[2], again[2];
