@@ -963,16 +963,18 @@ __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDi
         auto add_up = [&](int c0, int c1, int32_t *to) {
             const uint32_t *p = reinterpret_cast<const uint32_t *>(hist) + w;
             uint32_t even = 0, odd = 0;
-            int c = c0 + part;
-#pragma unroll 2
-            for (; c + 2 * parts < c1; c += 3 * parts) {
-                const uint32_t x = __ldg(p + c * 2 * words) + __ldg(p + (c + parts) * 2 * words) +
-                                   __ldg(p + (c + 2 * parts) * 2 * words);
-                even += x & 0x00FF00FFu;
-                odd += (x >> 8) & 0x00FF00FFu;
+            const int step = parts * 2 * words;
+            p += (c0 + part) * 2 * words;
+            int left = c1 - c0 - part;  // rows of this thread: every parts-th of them
+            for (; left > 5 * parts; left -= 6 * parts, p += 6 * step) {
+                const uint32_t x0 = __ldg(p), x1 = __ldg(p + step), x2 = __ldg(p + 2 * step), x3 = __ldg(p + 3 * step),
+                               x4 = __ldg(p + 4 * step), x5 = __ldg(p + 5 * step);
+                const uint32_t y = x0 + x1 + x2, z = x3 + x4 + x5;
+                even += (y & 0x00FF00FFu) + (z & 0x00FF00FFu);
+                odd += ((y >> 8) & 0x00FF00FFu) + ((z >> 8) & 0x00FF00FFu);
             }
-            for (; c < c1; c += parts) {
-                const uint32_t x = __ldg(p + c * 2 * words);
+            for (; left > 0; left -= parts, p += step) {
+                const uint32_t x = __ldg(p);
                 even += x & 0x00FF00FFu;
                 odd += (x >> 8) & 0x00FF00FFu;
             }
