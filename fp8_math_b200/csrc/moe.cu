@@ -807,9 +807,9 @@ BSQ_DEV void cta_scan(const int32_t *n, int E, int32_t *off, int *wsum) {
 // Pass 3.  Row of a slot = its expert's offset + the prefix of the blocks
 // before + the chunk's prefix in its block + the rank inside the chunk; the
 // rows past the last routed one repeat the first row's token.  A CTA takes
-// `span` chunks of one block; the last one also writes the offsets and the
-// loss.  (Laying the rows out by expert in shared memory, to write row_index
-// in runs, took 12 us more than the scattered writes at 131072x8 slots.)
+// `span` chunks of one block; one more writes the offsets and the loss.
+// (Laying the rows out by expert in shared memory, to write row_index in runs,
+// took 12 us more than the scattered writes at 131072x8 slots.)
 __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd, int E, int64_t nchunk, int span,
                                                           const uint8_t *__restrict__ hist,
                                                           const uint16_t *__restrict__ prefix,
@@ -822,7 +822,8 @@ __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd,
     __shared__ float sums[kRouteMaxExperts];
     __shared__ int wsum[8], first_chunk;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t blocks = gridDim.x, b = blockIdx.x;
+    const int64_t blocks = gridDim.x - 1, b = blockIdx.x;  // the last column's first CTA has no chunks
+    if (b == blocks && blockIdx.y > 0) return;
     const int64_t c0 = min(b * kBlock + blockIdx.y * span, nchunk);
     const int64_t c1 = max(c0, min(min(c0 + span, (b + 1) * kBlock), nchunk));
     const uint32_t k = kd.d, i0 = (uint32_t)(min(c0 * kChunk, T) * k);  // slots i0 .. i0 + here, below 2^31
@@ -878,7 +879,7 @@ __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd,
         for (int x = threadIdx.x; x < here; x += 256)
             if ((int64_t)i0 + x >= total) out.row_index[i0 + x] = token;
     }
-    if (b < blocks - 1 || blockIdx.y < gridDim.y - 1) return;
+    if (b < blocks) return;
     for (int e = threadIdx.x; e <= E; e += 256) {
         int none;
         if (e == E) all[E] = column_sum(count + E, E + 1, blocks, 0, &none);
@@ -1594,7 +1595,7 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
     // about three CTAs per SM: each adds up all blocks' counts
     const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(kBlock, 3 * num_sms / blocks));
     const int span = (kBlock + parts - 1) / parts;
-    return launch_dependent(route_place_kernel, dim3((unsigned)blocks, (kBlock + span - 1) / span), dim3(256), 0, s,
+    return launch_dependent(route_place_kernel, dim3((unsigned)blocks + 1, (kBlock + span - 1) / span), dim3(256), 0, s,
                             a.T, unit_div((uint32_t)a.topk), E, w.nchunk, span, (const uint8_t *)(a.ws + w.hist),
                             (const uint16_t *)prefix, (const int32_t *)count, (const float *)psum_block, out,
                             a.coef) != cudaSuccess;
