@@ -1304,16 +1304,16 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__rest
 }
 
 // ------------------------------------------------------------------ gated SiLU with an MXFP8 checkpoint
-// sigmoid(g) as r or e r with e = exp(-|g|), r = 1 / (1 + e): e never
-// overflows and r lies in [1/2, 1].  e is the square of 2^(-|g| log2(e) / 2),
-// so that its subnormal values come from an ordinary product.  Relative error
-// (13 + 2 |g|) 2^-24 at most, the |g| from the rounding of the exponent;
-// results are rounded to 2^-8.
-BSQ_DEV float sigmoid(float g) {
-    const float half = ex2(fabsf(g) * (-0.5f * kLog2e));
-    const float e = half * half;
-    const float r = rcp(1.0f + e);
-    return (g >= 0.0f ? 1.0f : e) * r;
+// sigmoid of a pair, 1 / (1 + 2^(-g log2 e)).  Relative error (9 + 2 |g|) 2^-24
+// at most, the |g| from the rounding of the exponent; results are rounded to
+// 2^-8.  2^x overflows to infinity, whose reciprocal is 0: a sigmoid below 2^-126
+// (g < -87.3) is 0.  (Keeping its subnormal values takes a branch-free form with
+// exp(-|g|) and a select, 3.5 instructions of 26 a value more.)
+BSQ_DEV f32x2 sigmoid2(f32x2 g) {
+    float a, b;
+    f2_unpack(f2_mul(g, f2_pack(-kLog2e, -kLog2e)), a, b);
+    f2_unpack(f2_add(f2_pack(ex2(a), ex2(b)), f2_pack(1.0f, 1.0f)), a, b);
+    return f2_pack(rcp(a), rcp(b));
 }
 
 // Larger of two bf16 pairs of magnitudes, lane by lane.
@@ -1391,8 +1391,10 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__r
         if (i >= n) continue;
 #pragma unroll
         for (int q = 0; q < 8; q++) {
-            const float g0 = bf16_lo(g[q]), g1 = bf16_hi(g[q]);
-            o[q] = pack_bf16(g0 * sigmoid(g0) * bf16_lo(v[q]), g1 * sigmoid(g1) * bf16_hi(v[q]));
+            const f32x2 gq = f2_pack(bf16_lo(g[q]), bf16_hi(g[q]));
+            float a, b;
+            f2_unpack(f2_mul(f2_mul(gq, sigmoid2(gq)), f2_pack(bf16_lo(v[q]), bf16_hi(v[q]))), a, b);
+            o[q] = pack_bf16(a, b);
             top = max_bf16x2(top, o[q] & kAbs2);
         }
         store16(h + r * ldh + c, o);
@@ -1444,21 +1446,18 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__
         }
 #pragma unroll
         for (int q = 0; q < 8; q++) {
-            float gg[2], vv[2], dx[2], dy[2], again[2];
-            f2_unpack(g[q], gg[0], gg[1]);
-            f2_unpack(v[q], vv[0], vv[1]);
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const float dd = e ? bf16_hi(d[q]) : bf16_lo(d[q]);
-                const float s = sigmoid(gg[e]), gs = gg[e] * s;
-                dy[e] = dd * gs;
-                // s (1 + g (1 - s)) = s + gs - gs s
-                dx[e] = dd * vv[e] * fmaf(gs, 1.0f - s, s);
-                again[e] = gs * vv[e];
+            const f32x2 dd = f2_pack(bf16_lo(d[q]), bf16_hi(d[q])), sg2 = sigmoid2(g[q]), gs = f2_mul(g[q], sg2);
+            float a, b;
+            f2_unpack(f2_mul(dd, gs), a, b);
+            y[q] = pack_bf16(a, b);
+            // s (1 + g (1 - s)) = s + gs (1 - s)
+            const f32x2 slope = f2_fma(gs, f2_sub(f2_pack(1.0f, 1.0f), sg2), sg2);
+            f2_unpack(f2_mul(f2_mul(dd, v[q]), slope), a, b);
+            x[q] = pack_bf16(a, b);
+            if (AGAIN) {
+                f2_unpack(f2_mul(gs, v[q]), a, b);
+                w[q] = pack_bf16(a, b);
             }
-            x[q] = pack_bf16(dx[0], dx[1]);
-            y[q] = pack_bf16(dy[0], dy[1]);
-            if (AGAIN) w[q] = pack_bf16(again[0], again[1]);
         }
         store16(du + r * lddu + c, x);
         store16(du + r * lddu + F + c, y);

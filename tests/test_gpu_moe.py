@@ -9,8 +9,8 @@ chain of operations, and one rounding of the output type (bf16: 2^-8).  An
 exponential e^d of d = x - max is formed as 2^(d log2 e): the roundings of the
 difference, of the product and of the constant are each |d| U in d, so 3 |d| U
 in e^d; ex2.approx adds 4 U (2^-22), rcp.approx 2 U, a product or sum 1 U per
-step.  In the sigmoid d = -|g| is exact, which leaves 2 |g| U, and e^d is the
-square of 2^(d log2 e / 2): 2 x 4 U and the product."""
+step.  In the sigmoid d = -g is exact, which leaves 2 |g| U; one below 2^-126 is
+0 there (its exponential overflows), which adds 2^-126 times what it multiplies."""
 import numpy as np
 import pytest
 import torch
@@ -336,15 +336,19 @@ def gate_input(M, F, seed):
 
 
 def swiglu_tol(u, want):
-    """The sigmoid (2 |g| + 9 for the exponential, 1 + e, the reciprocal 2, e r) and two products, all U; bf16's
-    rounding, whose subnormal half step is 2^-134."""
-    return (B + (2 * np.minimum(abs(u[:, :u.shape[1] // 2]), 104) + 15) * U) * abs(want) + 1e-40
+    """The sigmoid (2 |g| + 4 for the exponential, 1 + e, the reciprocal 2) and two products, all U; bf16's rounding,
+    whose subnormal half step is 2^-134; a sigmoid of 0."""
+    F = u.shape[1] // 2
+    g, v = np.minimum(abs(u[:, :F]), 104), abs(u[:, F:])
+    return (B + (2 * g + 10) * U) * abs(want) + 1e-40 + 2.0 ** -126 * g * v
 
 
-def swiglu_bwd_tol(u, mag, want):
+def swiglu_bwd_tol(dh, u, mag, want):
     """The same sigmoid, 1 - s (its error is that of s), and five products and sums, relative to mag."""
-    g = np.minimum(abs(u[:, :u.shape[1] // 2]), 104)
-    t = (2 * (2 * np.concatenate([g, g], 1) + 13) + 6) * U * mag
+    F = u.shape[1] // 2
+    g, v = np.minimum(abs(u[:, :F]), 104), abs(u[:, F:])
+    t = (2 * (2 * np.concatenate([g, g], 1) + 7) + 6) * U * mag
+    t = t + 2.0 ** -126 * np.concatenate([abs(dh) * v * (1 + g), abs(dh) * g], 1)
     return t + B * (abs(want) + t) + 1e-40
 
 
@@ -379,7 +383,7 @@ def test_swiglu_ckpt_bwd(M, F, again):
     du, h = api.swiglu_ckpt_bwd(wide, codes, sf, out=out)
     with np.errstate(over="ignore"):
         want, mag = ref.swiglu_bwd(n64(dh), v)
-        tol = swiglu_bwd_tol(v, mag, want)
+        tol = swiglu_bwd_tol(n64(dh), v, mag, want)
         fine = np.isfinite(want) & (abs(want) < 1e38)  # 3e38 times dh passes bf16's range
         got = np.where(fine, n64(du), 0)
         want, tol = np.where(fine, want, 0), np.where(fine, tol, 0)
@@ -567,7 +571,7 @@ def test_layer_forward_and_backward():
     assert (n64(o["dy"][n:]) == 0).all()
     v = decode8(o["uc"][:n], o["us"])
     want, mag = ref.swiglu_bwd(n64(o["dh"][:n]), v)
-    within(n64(o["du"][:n]), want, swiglu_bwd_tol(v, mag, want), "du")
+    within(n64(o["du"][:n]), want, swiglu_bwd_tol(n64(o["dh"][:n]), v, mag, want), "du")
     want = ref.swiglu(v)
     within(n64(o["again"][:n]), want, swiglu_tol(v, want), "h again")
     want, mag = ref.combine(n64(o["dxr"][:n]), rows, None)
