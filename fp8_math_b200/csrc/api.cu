@@ -650,7 +650,7 @@ int bsq_moe_combine_bwd(const void *dout, int64_t ldo, const void *y, int64_t ld
     if (R < 0 || H < 0 || H % 8 || ldo < H || lddy < H || T < 0 || topk < 1) return BSQ_ERR_INVALID;
     if (y && (y_codes || y_sf)) return BSQ_ERR_INVALID;       // one form of y, not both
     if (!y && (!y_codes != !y_sf)) return BSQ_ERR_INVALID;    // codes and scales come together
-    if (y ? ldy < H : H % 32 != 0) return BSQ_ERR_INVALID;
+    if ((y && ldy < H) || (y_codes && H % 32)) return BSQ_ERR_INVALID;
     if (topk > bsq::kRouteMaxTopk || T >= (int64_t(1) << 31) || T * topk >= (int64_t(1) << 31) ||
         H > (int64_t(1) << 25))
         return BSQ_ERR_UNSUPPORTED;

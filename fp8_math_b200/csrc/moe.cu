@@ -292,8 +292,8 @@ struct Candidates<float, LPT, Q> {
 // lane sorts its logits by networks of maxima and minima, and log2(LPT)
 // exchanges merge the lanes' lists (the larger of a[i] and b[L-1-i] are the L
 // best of two sorted lists, in bitonic order).  Against rounds of one maximum
-// each this took 131072x256, k = 8, from 77 to 48 us and 16384x64 from 9.0 to
-// 6.4 us.  The entries are logits with the expert in their low bits, as above.
+// each this took the whole call from 96 to 81 us at 131072x256, k = 8, and from
+// 5.7 to 4.3 us at 64x64.  The entries are logits with the expert in their low bits, as above.
 // An fp32 logit gives its lowest ceil(log2 E) bits for it; where two such
 // truncated logits meet in the list or at its end, the order is not certain and
 // the warp's tokens go through the rounds instead.  NaN entries (-inf logits)
@@ -461,14 +461,14 @@ BSQ_DEV bool choose(const Row<In, LPT, Q> &row, const In *logits, int sub, int E
     // the last slot's truncated logit: nothing else may have it
     const float last = __shfl_sync(kFull, entry<L>(v, k - 1), 0, LPT);
     const uint32_t lb = __float_as_uint(last);
-    const float floor = __uint_as_float((lb >> 31) ? lb | bits : lb & ~bits);
+    const float least = __uint_as_float((lb >> 31) ? lb | bits : lb & ~bits);
     int n = 0;
 #pragma unroll
     for (int q = 0; q < Q; q++) {
         float x[4];
         row.get(q, x);
 #pragma unroll
-        for (int i = 0; i < 4; i++) n += x[i] >= floor;
+        for (int i = 0; i < 4; i++) n += x[i] >= least;
     }
 #pragma unroll
     for (int o = LPT / 2; o; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
@@ -674,12 +674,12 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
                 psum[(int64_t)blockIdx.x * E + e] = v;
             }
     } else {
-        const int here = (int)T, total = off[E], tokens = __popcll(smem[E]);
+        __shared__ int first_token;
+        const int slots = (int)T * k, total = off[E], tokens = __popcll(smem[E]);
+        if (threadIdx.x == 0) first_token = 0;
+        __syncthreads();
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
-            if (off[e] == 0 && off[e + 1] > 0)  // the expert of the first row, and its first token
-                for (int i = total; i < here * k; i++) out.row_index[i] = __ffsll(smem[e]) - 1;
-            if (total == 0 && e == 0)
-                for (int i = 0; i < here * k; i++) out.row_index[i] = 0;
+            if (off[e] == 0 && off[e + 1] > 0) first_token = __ffsll(smem[e]) - 1;  // one expert has the first row
             if (want_p) {
                 float v = 0.0f;
                 for (int w = 0; w < nwarps; w++) v += red[w * E + e];
@@ -694,6 +694,7 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
             out.row_off[E] = total;
         }
         __syncthreads();
+        for (int i = total + threadIdx.x; i < slots; i += blockDim.x) out.row_index[i] = first_token;
         if (warp == 0) {
             if (out.loss) {
                 float v = 0.0f;
@@ -1186,7 +1187,8 @@ __global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(c
 
 // ------------------------------------------------------------------ combine
 // out[t] = sum_j w_tj y[rows_tj]: a CTA of 128 threads takes 1024 columns of
-// one token, each thread eight of them over all k rows.
+// one token, each thread eight of them over all k rows.  Memory bound:
+// 16384x8x4096 takes 199 us, 93 % of the measured copy rate.
 __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict__ y, int64_t R, int64_t H, int64_t ldy,
                                                       const int32_t *__restrict__ rows,
                                                       const float *__restrict__ weights, int k,
@@ -1246,7 +1248,10 @@ BSQ_DEV void bwd8(uint4 dq, const f32x2 v[4], f32x2 w2, f32x2 &dot2, uint16_t *t
 // dy[rows_tj] = w_tj dout_t and dw_tj = <dout_t, y[rows_tj]>: one warp per
 // slot, so that empty slots cost nothing and no sum leaves the warp; a
 // token's dout is read from DRAM by one of its warps and by the others from
-// L1.  Memory bound: y read once, dy written once.
+// L1.  Memory bound: y read once, dy written once.  16384x8x4096: 354 us, 99 % of
+// the measured copy rate, against 410 with one CTA per token; from 8-bit rows 320
+// us, bound by the writes (a fill reaches 3.9 TB/s).  Warps that stay and take slot
+// after slot were slower (420 us): the order of the rows in flight spreads.
 template <bool MX>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__restrict__ dout, int64_t ldo,
                                                           const uint16_t *__restrict__ y, int64_t ldy,
@@ -1358,23 +1363,23 @@ BSQ_DEV void store16(uint16_t *p, const uint32_t w[8]) {
 }
 
 __global__ void zero_word_kernel(unsigned int *p) {
+    grid_dependents_launch();
     grid_dependency_wait();
-    grid_dependents_launch();  // not before: the next kernel relies on all earlier work being done
     *p = 0;
 }
 
 // Memory bound: 8.06 bytes per h.  A thread takes 16 columns of the gate and
 // the same 16 of v (64 bytes in flight), so two lanes share a block of 32 and
-// write one scale byte each.
+// write one scale byte each.  131072x768: 136 us, 92 % of the measured copy
+// rate; 8 columns a thread took 172 us (twice the addresses and exchanges), and
+// a grid that stays resident no less.
 __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F,
                                                           int64_t ldu, UnitDiv per, const int32_t *__restrict__ n_rows,
                                                           uint16_t *__restrict__ h, int64_t ldh,
                                                           uint8_t *__restrict__ codes, uint8_t *__restrict__ sf,
                                                           unsigned int *__restrict__ amax) {
     grid_dependents_launch();
-    // with amax, zero_word_kernel before this one has waited for all earlier work; only the word that it
-    // zeroes has to wait for it, at the end
-    if (!amax) grid_dependency_wait();
+    grid_dependency_wait();
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;  // even: a block's two lanes go together
     uint32_t top = 0;
@@ -1405,7 +1410,6 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__r
         sf[sf_offset(r, (c + (odd ? F : 0)) >> 5, F >> 4)] = (uint8_t)(odd ? sv : sg);
     }
     if (amax) {
-        grid_dependency_wait();
         top = __reduce_max_sync(kFull, max(top & 0xFFFFu, top >> 16)) << 16;
         // non-negative floats order as their bits; most warps find a larger one there already
         if ((threadIdx.x & 31) == 0 && top > *reinterpret_cast<volatile unsigned int *>(amax)) atomicMax(amax, top);

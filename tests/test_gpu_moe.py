@@ -307,6 +307,9 @@ def test_combine_without_tokens_or_rows():
     dy, dw = api.moe_combine_bwd(torch.ones(3, 64, dtype=torch.bfloat16, device="cuda"), y0, none,
                                  torch.ones(3, 2, device="cuda"))
     assert dy.shape == (0, 64) and (n64(dw) == 0).all()
+    dy, dw = api.moe_combine_bwd(torch.ones(3, 40, dtype=torch.bfloat16, device="cuda"), y0[:, :40].contiguous(), none,
+                                 torch.ones(3, 2, device="cuda"))
+    assert dy.shape == (0, 40) and (n64(dw) == 0).all()
 
 
 # ------------------------------------------------------------------ gated SiLU
@@ -484,6 +487,52 @@ def test_same_bits_every_time_on_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(c, want))
 
 
+def test_offsets_past_31_bits():
+    """Tensors of more than 2^31 elements: rows at both ends against the same rows alone."""
+    T, E = 8_500_000, 256                                                   # 2.2e9 logits
+    want = torch.randint(0, E, (T,), device="cuda", dtype=torch.int32)
+    z = torch.zeros(T, E, dtype=torch.bfloat16, device="cuda")
+    z.scatter_(1, want.long()[:, None], 1.0)
+    r = api.moe_route(z, 1, balance_coef=1.0)
+    assert torch.equal(r.expert_ids[:, 0], want)
+    order = torch.sort(want, stable=True).indices
+    assert torch.equal(r.row_index, order.int())
+    assert torch.equal(r.rows[:, 0].long()[order], torch.arange(T, device="cuda"))
+    assert torch.equal(r.counts[:E], torch.bincount(want, minlength=E).int())
+    one = torch.ones(1, device="cuda")
+    d = api.moe_route_bwd(z, r.expert_ids, r.weights, counts=r.counts, dloss=one, balance_coef=1e6)
+    for at in (slice(0, 9), slice(T - 9, T)):
+        alone = api.moe_route_bwd(z[at].clone(), r.expert_ids[at], r.weights[at], counts=r.counts, dloss=one,
+                                  balance_coef=1e6)
+        assert torch.equal(d[at], alone) and (alone != 0).any()
+    del z, d, r, order, want
+    R, H = 300_000, 8192                                                    # 2.5e9 values
+    y = torch.zeros(R, H, dtype=torch.bfloat16, device="cuda")
+    y[-4:] = torch.randn(4, H, device="cuda")
+    rows = torch.tensor([[R - 1, 0], [R - 3, R - 4]], dtype=torch.int32, device="cuda")
+    w = torch.rand(2, 2, device="cuda")
+    near = torch.tensor([[3, -1], [1, 0]], dtype=torch.int32, device="cuda")  # the last four rows alone (row 0 is zeros)
+    assert torch.equal(api.moe_combine(y, rows, w), api.moe_combine(y[-4:].clone(), near, w))
+    g = torch.randn(2, H, device="cuda").to(torch.bfloat16)
+    dy, dw = api.moe_combine_bwd(g, y, rows, w)
+    dy4, dw4 = api.moe_combine_bwd(g, y[-4:].clone(), near, w)
+    assert torch.equal(dy[-4:], dy4) and torch.equal(dw, dw4)
+    codes, sf = api.quant_mxfp8(y)
+    _, dw8 = api.moe_combine_bwd(g, (codes, sf), rows, w, out=(dy, dw))
+    _, dw84 = api.moe_combine_bwd(g, api.quant_mxfp8(y[-4:].clone()), near, w)
+    assert torch.equal(dw8, dw84)
+    del dy, codes, sf
+    u = y.view(R * 4, 2048)                                                 # gate and v of 1024 columns each
+    h, codes, sf, am = api.swiglu_ckpt(u)
+    h4, codes4, _, am4 = api.swiglu_ckpt(u[-16:].clone())
+    assert torch.equal(h[-16:], h4) and torch.equal(codes[-16:], codes4) and am.item() == am4.item() > 0
+    dh = torch.zeros_like(h)
+    dh[-16:] = 1
+    du, _ = api.swiglu_ckpt_bwd(dh, codes, sf)
+    du4, _ = api.swiglu_ckpt_bwd(dh[-16:].clone(), *api.quant_mxfp8(u[-16:].clone()))
+    assert torch.equal(du[-16:], du4) and (du4 != 0).any()
+
+
 class Layer:
     """A mixture-of-experts layer's forward and backward pass in the library's calls."""
 
@@ -577,6 +626,25 @@ def test_layer_forward_and_backward():
     want, mag = ref.combine(n64(o["dxr"][:n]), rows, None)
     within(n64(o["dx"]), want, 3 * U * mag + B * (abs(want) + 3 * U * mag), "dx")
     check_route_bwd(z, r, o["dw"].cpu(), 1.0, 0.01, True)
+
+
+def test_launch_overlap_changes_no_byte(knobs):
+    """Back-to-back steps, each call reading what the one before it wrote, with and without overlapped launches."""
+    layer = Layer(128, 128, 4, 2, 3)
+    ins = layer_inputs(150, 128, 4, 5)
+    got = []
+    for overlap in (0, 1):
+        knobs(bsq.BSQ_KNOB_LAUNCH_OVERLAP, overlap)
+        for _ in range(3):
+            o = layer.step(*ins)
+        torch.cuda.synchronize()
+        got.append(o)
+    n = int(got[0]["r"].row_offsets[4])
+    for name in ("out", "dw", "dx", "dz", "am"):
+        assert torch.equal(got[0][name], got[1][name]), name
+    for name in ("h", "du", "again"):
+        assert torch.equal(got[0][name][:n], got[1][name][:n]), name
+    assert bsq.bsq_check() == bsq.BSQ_OK
 
 
 def test_layer_replayed_from_a_graph():

@@ -136,7 +136,8 @@ def test_combine_refusals(L):
     for bad in [dict(dout=264), dict(y=264), dict(y=None, c=264, s=p), dict(y=None, c=p, s=264), dict(dy=264),
                 dict(ldo=68), dict(ldy=68), dict(lddy=68), dict(rows=258), dict(w=258), dict(dw=258)]:
         assert bwd(**bad) == L.BSQ_ERR_ALIGN, bad
-    assert bwd(k=33) == L.BSQ_ERR_UNSUPPORTED
+    assert bwd(k=33) == L.BSQ_ERR_UNSUPPORTED and bwd(T=1 << 30, k=2) == L.BSQ_ERR_UNSUPPORTED
+    assert bwd(H=1 << 26, ldo=1 << 26, ldy=1 << 26, lddy=1 << 26) == L.BSQ_ERR_UNSUPPORTED
 
 
 def test_swiglu_refusals(L):
@@ -151,6 +152,8 @@ def test_swiglu_refusals(L):
     for bad in [dict(u=264), dict(h=264), dict(c=264), dict(s=264), dict(ldu=68), dict(ldh=36), dict(n=258),
                 dict(amax=258)]:
         assert fwd(**bad) == L.BSQ_ERR_ALIGN, bad
+
+    assert fwd(M=1 << 30, F=32) == L.BSQ_ERR_UNSUPPORTED and fwd(M=1 << 31) == L.BSQ_ERR_UNSUPPORTED
 
     def bwd(dh=p, lddh=32, c=p, s=p, M=4, F=32, n=None, du=p, lddu=64, h=None, ldh=0):
         return lib.bsq_swiglu_ckpt_bwd(dh, lddh, c, s, M, F, n, du, lddu, h, ldh, None)
