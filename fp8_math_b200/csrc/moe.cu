@@ -1188,7 +1188,7 @@ __global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(c
 // ------------------------------------------------------------------ combine
 // out[t] = sum_j w_tj y[rows_tj]: a CTA of 128 threads takes 1024 columns of
 // one token, each thread eight of them over all k rows.  Memory bound:
-// 16384x8x4096 takes 199 us, 93 % of the measured copy rate.
+// 16384x8x4096 takes 185 us, the measured copy rate (199 us with one row in flight).
 __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict__ y, int64_t R, int64_t H, int64_t ldy,
                                                       const int32_t *__restrict__ rows,
                                                       const float *__restrict__ weights, int k,
@@ -1198,20 +1198,37 @@ __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict
     const int64_t t = blockIdx.x;
     const int64_t c = ((int64_t)blockIdx.y * 128 + threadIdx.x) * 8;
     if (c >= H) return;
-    float acc[8];
+    f32x2 acc[4];
 #pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] = 0.0f;
-    for (int j = 0; j < k; j++) {
-        const int64_t r = __ldg(rows + t * k + j);
-        if (r < 0 || r >= R) continue;
-        const float w = weights ? __ldg(weights + t * k + j) : 1.0f;
-        float v[8];
-        load8_bf16(y + r * ldy + c, v);
+    for (int i = 0; i < 4; i++) acc[i] = f2_pack(0.0f, 0.0f);
+    rows += t * k;
+    if (weights) weights += t * k;
+    for (int j0 = 0; j0 < k; j0 += 4) {  // four rows in flight
+        uint4 q[4];
+        float w[4];
 #pragma unroll
-        for (int i = 0; i < 8; i++) acc[i] += w * v[i];
+        for (int j = 0; j < 4; j++) {
+            const int64_t r = j0 + j < k ? __ldg(rows + j0 + j) : -1;
+            const bool has = r >= 0 && r < R;
+            w[j] = !has ? 0.0f : weights ? __ldg(weights + j0 + j) : 1.0f;
+            q[j] = has ? __ldg(reinterpret_cast<const uint4 *>(y + r * ldy + c)) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const uint32_t v[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+            const f32x2 w2 = f2_pack(w[j], w[j]);
+#pragma unroll
+            for (int i = 0; i < 4; i++) acc[i] = f2_fma(w2, f2_pack(bf16_lo(v[i]), bf16_hi(v[i])), acc[i]);
+        }
     }
-    *reinterpret_cast<uint4 *>(out + t * ldo + c) = make_uint4(pack_bf16(acc[0], acc[1]), pack_bf16(acc[2], acc[3]),
-                                                               pack_bf16(acc[4], acc[5]), pack_bf16(acc[6], acc[7]));
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        float lo, hi;
+        f2_unpack(acc[i], lo, hi);
+        o[i] = pack_bf16(lo, hi);
+    }
+    *reinterpret_cast<uint4 *>(out + t * ldo + c) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // 2^(code - 127) of an E8M0 code (0: 2^-127, a subnormal).
