@@ -759,13 +759,14 @@ __global__ void __launch_bounds__(256) route_block_kernel(const uint8_t *__restr
 }
 
 // Sum of n values `stride` apart, 16 loads in flight; *part that of the first m.
+// (n stride < 2^31: a block of 4096 tokens has at most 1025 values.)
 template <typename V>
-BSQ_DEV V column_sum(const V *p, int64_t stride, int64_t n, int64_t m, V *part) {
+BSQ_DEV V column_sum(const V *p, int stride, int n, int m, V *part) {
     V s = 0, first = 0;
-    for (int64_t b = 0; b < n; b += 16) {
+    for (int b = 0; b < n; b += 16, p += 16 * stride) {
         V v[16];
 #pragma unroll
-        for (int i = 0; i < 16; i++) v[i] = b + i < n ? __ldg(p + (b + i) * stride) : V(0);
+        for (int i = 0; i < 16; i++) v[i] = b + i < n ? __ldg(p + i * stride) : V(0);
 #pragma unroll
         for (int i = 0; i < 16; i++) {
             s += v[i];
@@ -832,7 +833,7 @@ __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd,
     const uint16_t *at = prefix + c0 * E;
     for (int e = threadIdx.x; e < E; e += 256) {
         int before;
-        all[e] = column_sum(count + e, E + 1, blocks, b, &before);
+        all[e] = column_sum(count + e, E + 1, (int)blocks, (int)b, &before);
         base[e] = before;
     }
     __syncthreads();
@@ -883,12 +884,12 @@ __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd,
     if (b < blocks) return;
     for (int e = threadIdx.x; e <= E; e += 256) {
         int none;
-        if (e == E) all[E] = column_sum(count + E, E + 1, blocks, 0, &none);
+        if (e == E) all[E] = column_sum(count + E, E + 1, (int)blocks, 0, &none);
         out.counts[e] = all[e];
         out.row_off[e] = off[e];
         if (psum_block && e < E) {
             float part;
-            sums[e] = column_sum(psum_block + e, E, blocks, 0, &part);
+            sums[e] = column_sum(psum_block + e, E, (int)blocks, 0, &part);
             if (out.prob_sums) out.prob_sums[e] = sums[e];
         }
     }
