@@ -104,7 +104,7 @@ struct Row<uint16_t, LPT, Q> {
             if (!live || e >= E) continue;
             if (vec) {
                 w[q] = __ldg(reinterpret_cast<const uint2 *>(row + e));
-            } else {
+            } else {  // (32-bit words and a shift were slower: neighbouring rows part ways)
                 uint32_t v[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++) v[i] = e + i < E ? (uint32_t)__ldg(row + e + i) : 0xFF80u;
@@ -1037,6 +1037,21 @@ BSQ_DEV void store4(uint16_t *p, const float d[4]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]));
 }
 
+// A row of E values by LPT lanes, at any alignment of whole elements.
+template <int LPT>
+BSQ_DEV void store_row(float *to, const float *row, int E, int sub) {
+    for (int e = sub; e < E; e += LPT) to[e] = row[e];
+}
+template <int LPT>
+BSQ_DEV void store_row(uint16_t *to, const float *row, int E, int sub) {
+    const int mid = (reinterpret_cast<uintptr_t>(to) & 2u) ? 1 : 0;  // words of elements (2i - mid, 2i + 1 - mid)
+    for (int e = 2 * sub - mid; e < E; e += 2 * LPT) {
+        if (e >= 0 && e + 1 < E) *reinterpret_cast<uint32_t *>(to + e) = pack_bf16(row[e], row[e + 1]);
+        else if (e >= 0) store_logit(to + e, row[e]);
+        else store_logit(to, row[0]);
+    }
+}
+
 // CTAs per SM, and the grid is no larger: five at 48 registers where a lane's
 // logits leave that many free, six where the softmax is not needed (shared
 // memory).  131072x256 takes 50 us with eight CTAs per SM in turns, 35 with three.
@@ -1063,7 +1078,8 @@ __global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(c
     grid_dependents_launch();
     grid_dependency_wait();
     constexpr int kGroups = 32 / LPT, kCols = 4 * LPT * Q;
-    __shared__ __align__(16) float own_rows[8 * kGroups][kCols];
+    // rows 32 bytes apart in the banks, for the groups' reads of single values
+    __shared__ __align__(16) float own_rows[8 * kGroups][kCols + 8];
     __shared__ __align__(16) float bias[NEED_P ? kCols : 4];
     const int lane = threadIdx.x & 31, sub = lane % LPT;
     const int group = threadIdx.x / LPT;
@@ -1164,15 +1180,21 @@ __global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(c
                 d[q][2] = o.z;
                 d[q][3] = o.w;
             }
-            if (!in || e >= E) continue;
-            In *to = dlogits + t * ldd + e;
-            if (vec) {
-                store4(to, d[q]);
-            } else {
+            if (vec && in && e < E) store4(dlogits + t * ldd + e, d[q]);
+        }
+        if (!vec) {  // the row's values go through its shared memory, to be written side by side
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (e + i < E) store_logit(to + i, d[q][i]);
-            }
+            for (int q = 0; q < Q; q++)
+                *reinterpret_cast<float4 *>(own_row + 4 * (q * LPT + sub)) =
+                    make_float4(d[q][0], d[q][1], d[q][2], d[q][3]);
+            __syncwarp();
+            if (in) store_row<LPT>(dlogits + t * ldd, own_row, E, sub);
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < Q; q++)
+                *reinterpret_cast<float4 *>(own_row + 4 * (q * LPT + sub)) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            __syncwarp();
+            continue;
         }
         __syncwarp();
         if (dweights) {
