@@ -39,7 +39,7 @@
  *  - Behaviour is selected by the arguments alone; the library reads no
  *    environment variable.  bsq_debug_kernel_choice() can force one of two
  *    equivalent kernels for tests and tuning (results are identical).
- *  - CUDA graphs: the quantize and GEMM entry points may be called on a
+ *  - CUDA graphs: the quantize, GEMM and MoE entry points may be called on a
  *    stream under capture once the same calls have run once outside capture
  *    on that device (the first call creates the per-device error word and
  *    sets kernel attributes).  Under capture an amax + quantize pair is
