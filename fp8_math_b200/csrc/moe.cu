@@ -27,7 +27,6 @@ BSQ_DEV uint32_t pack_bf16(float lo, float hi) {
 }
 BSQ_DEV float load_logit(const float *p) { return __ldg(p); }
 BSQ_DEV float load_logit(const uint16_t *p) { return __uint_as_float((uint32_t)__ldg(p) << 16); }
-BSQ_DEV void store_logit(float *p, float v) { *p = v; }
 BSQ_DEV void store_logit(uint16_t *p, float v) { *p = (uint16_t)(pack_bf16(v, 0.0f) & 0xFFFFu); }
 
 // a * b + c on an fp32 pair
@@ -514,13 +513,15 @@ struct RouteOut {
 };
 
 // Pass 1.  A CTA takes chunks of kChunk consecutive tokens in turn, LPT lanes a
-// token; the sums of probabilities stay in its registers.  The softmax sum runs over the same registers as the choice.  The chosen experts
-// go into one 64-bit mask of tokens per expert, whose population count is the
-// chunk's count and whose bits below a token are that token's rank in the
-// chunk: the order "by expert, then token" needs no sort.  Row E of the counts
-// is the number of tokens with at least one expert.  Where the chunk is all
-// there is, the CTA finishes the call (offsets, rows, loss).  L: k <= L by
-// sorted lists; 0: rounds for any k.
+// token; the sums of probabilities stay in its registers.  The softmax sum runs
+// over the same registers as the choice.  The chosen experts go into one 64-bit
+// mask of tokens per expert, whose population count is the chunk's count and
+// whose bits below a token are that token's rank in the chunk: the order "by
+// expert, then token" needs no sort.  Row E of the counts is the number of tokens
+// with at least one expert.  Where the chunk is all there is, the CTA finishes
+// the call (offsets, rows, loss).  L: k <= L by sorted lists; 0: rounds for any k.
+// 131072x256, k = 8: 46 of the call's 63 us, bound by instructions (235 per token;
+// minima and maxima run at half rate).
 template <typename In, int LPT, int Q, int L>
 __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                          int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
@@ -716,7 +717,8 @@ constexpr int kBlock = 64, kRun = kBlock / 8;
 
 __global__ void __launch_bounds__(256) route_block_kernel(const uint8_t *__restrict__ hist,
                                                           const float *__restrict__ psum, int64_t rows, int64_t nchunk,
-                                                          int E, uint16_t *__restrict__ prefix, int32_t *__restrict__ count,
+                                                          int E, uint16_t *__restrict__ prefix,
+                                                          int32_t *__restrict__ count,
                                                           float *__restrict__ psum_block) {
     grid_dependents_launch();
     grid_dependency_wait();
@@ -913,7 +915,8 @@ constexpr int kSmallHist = 48 * 1024, kSmallChunks = 512;
 
 __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDiv kd, int E, int nchunk,
                                                                UnitDiv wd, const uint8_t *__restrict__ hist,
-                                                               const float *__restrict__ psum, int64_t rows, RouteOut out,
+                                                               const float *__restrict__ psum, int64_t rows,
+                                                               RouteOut out,
                                                                float coef) {
     grid_dependents_launch();
     grid_dependency_wait();
@@ -1032,7 +1035,9 @@ __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDi
 }
 
 // ------------------------------------------------------------------ router, backward
-BSQ_DEV void store4(float *p, const float d[4]) { *reinterpret_cast<float4 *>(p) = make_float4(d[0], d[1], d[2], d[3]); }
+BSQ_DEV void store4(float *p, const float d[4]) {
+    *reinterpret_cast<float4 *>(p) = make_float4(d[0], d[1], d[2], d[3]);
+}
 BSQ_DEV void store4(uint16_t *p, const float d[4]) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]));
 }
@@ -1068,13 +1073,11 @@ constexpr int bwd_ctas() {
 // lanes that hold those experts through a row of shared memory per token,
 // which is zero between tokens.
 template <typename In, int LPT, int Q, bool NEED_P>
-__global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
-                                                        int vec, int k, int renorm, const int32_t *__restrict__ ids,
-                                                        const float *__restrict__ weights,
-                                                        const float *__restrict__ dweights,
-                                                        const int32_t *__restrict__ counts, float coef,
-                                                        const float *__restrict__ dloss, In *__restrict__ dlogits,
-                                                        int64_t ldd) {
+__global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>())
+    route_bwd_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl, int vec, int k, int renorm,
+                     const int32_t *__restrict__ ids, const float *__restrict__ weights,
+                     const float *__restrict__ dweights, const int32_t *__restrict__ counts, float coef,
+                     const float *__restrict__ dloss, In *__restrict__ dlogits, int64_t ldd) {
     grid_dependents_launch();
     grid_dependency_wait();
     constexpr int kGroups = 32 / LPT, kCols = 4 * LPT * Q;
@@ -1133,7 +1136,8 @@ __global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(c
             if (has) own_row[e0] = w0 * (a0 - all);
             for (int j = LPT; sub + j < k; j += LPT) {
                 const int e = in ? __ldg(ids + slot + j) : -1;
-                if ((unsigned)e < (unsigned)E) own_row[e] = __ldg(weights + slot + j) * (__ldg(dweights + slot + j) - all);
+                if ((unsigned)e < (unsigned)E)
+                    own_row[e] = __ldg(weights + slot + j) * (__ldg(dweights + slot + j) - all);
             }
         }
         float d[Q][4], sub_all = 0.0f, inv = 0.0f;
@@ -1212,6 +1216,7 @@ __global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>()) route_bwd_kernel(c
 // out[t] = sum_j w_tj y[rows_tj]: a CTA of 128 threads takes 1024 columns of
 // one token, each thread eight of them over all k rows.  Memory bound:
 // 16384x8x4096 takes 185 us, the measured copy rate (199 us with one row in flight).
+template <int B>
 __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict__ y, int64_t R, int64_t H, int64_t ldy,
                                                       const int32_t *__restrict__ rows,
                                                       const float *__restrict__ weights, int k,
@@ -1226,18 +1231,18 @@ __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict
     for (int i = 0; i < 4; i++) acc[i] = f2_pack(0.0f, 0.0f);
     rows += t * k;
     if (weights) weights += t * k;
-    for (int j0 = 0; j0 < k; j0 += 4) {  // four rows in flight
-        uint4 q[4];
-        float w[4];
+    for (int j0 = 0; j0 < k; j0 += B) {  // B rows in flight
+        uint4 q[B];
+        float w[B];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int j = 0; j < B; j++) {
             const int64_t r = j0 + j < k ? __ldg(rows + j0 + j) : -1;
             const bool has = r >= 0 && r < R;
             w[j] = !has ? 0.0f : weights ? __ldg(weights + j0 + j) : 1.0f;
             q[j] = has ? __ldg(reinterpret_cast<const uint4 *>(y + r * ldy + c)) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
+        for (int j = 0; j < B; j++) {
             const uint32_t v[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
             const f32x2 w2 = f2_pack(w[j], w[j]);
 #pragma unroll
@@ -1288,12 +1293,13 @@ BSQ_DEV void bwd8(uint4 dq, const f32x2 v[4], f32x2 w2, f32x2 &dot2, uint16_t *t
 // dy[rows_tj] = w_tj dout_t and dw_tj = <dout_t, y[rows_tj]>: one warp per
 // slot, so that empty slots cost nothing and no sum leaves the warp; a
 // token's dout is read from DRAM by one of its warps and by the others from
-// L1.  Memory bound: y read once, dy written once.  16384x8x4096: 354 us, 99 % of
-// the measured copy rate, against 410 with one CTA per token; from 8-bit rows 320
-// us, bound by the writes (a fill reaches 3.9 TB/s).  Warps that stay and take slot
-// after slot were slower (420 us): the order of the rows in flight spreads.
+// L1.  Memory bound: y read once, dy written once.  16384x8x4096: 351 us, the
+// measured copy rate, against 410 with one CTA per token (354 with eight warps a
+// CTA instead of four); from 8-bit rows 315 us, bound by the writes (a fill
+// reaches 3.9 TB/s).  Warps that stay and take slot after slot were slower (420
+// us): the order of the rows in flight spreads.
 template <bool MX>
-__global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__restrict__ dout, int64_t ldo,
+__global__ void __launch_bounds__(128) combine_bwd_kernel(const uint16_t *__restrict__ dout, int64_t ldo,
                                                           const uint16_t *__restrict__ y, int64_t ldy,
                                                           const uint8_t *__restrict__ codes,
                                                           const uint8_t *__restrict__ sf, int64_t R, int64_t H,
@@ -1303,7 +1309,7 @@ __global__ void __launch_bounds__(256) combine_bwd_kernel(const uint16_t *__rest
                                                           float *__restrict__ dweights) {
     grid_dependents_launch();
     grid_dependency_wait();
-    const uint32_t slot = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const uint32_t slot = blockIdx.x * 4 + (threadIdx.x >> 5);
     if (slot >= slots) return;
     const int lane = threadIdx.x & 31;
     const int64_t r = __ldg(rows + slot);
@@ -1408,23 +1414,24 @@ __global__ void zero_word_kernel(unsigned int *p) {
     *p = 0;
 }
 
+constexpr int kGlu = 128;  // threads of a gated SiLU CTA; 256: forward 135 us instead of 131
+
 // Memory bound: 8.06 bytes per h.  A thread takes 16 columns of the gate and
 // the same 16 of v (64 bytes in flight), so two lanes share a block of 32 and
-// write one scale byte each.  131072x768: 136 us, 92 % of the measured copy
+// write one scale byte each.  131072x768: 131 us, 95 % of the measured copy
 // rate; 8 columns a thread took 172 us (twice the addresses and exchanges), and
 // a grid that stays resident no less.
-__global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F,
-                                                          int64_t ldu, UnitDiv per, const int32_t *__restrict__ n_rows,
-                                                          uint16_t *__restrict__ h, int64_t ldh,
-                                                          uint8_t *__restrict__ codes, uint8_t *__restrict__ sf,
-                                                          unsigned int *__restrict__ amax) {
+__global__ void __launch_bounds__(kGlu, 1024 / kGlu)
+    swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F, int64_t ldu, UnitDiv per,
+                       const int32_t *__restrict__ n_rows, uint16_t *__restrict__ h, int64_t ldh,
+                       uint8_t *__restrict__ codes, uint8_t *__restrict__ sf, unsigned int *__restrict__ amax) {
     grid_dependents_launch();
     grid_dependency_wait();
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;  // even: a block's two lanes go together
     uint32_t top = 0;
     const int64_t round = (n + 31) & ~int64_t(31);  // the shuffle wants whole warps
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < round; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * kGlu + threadIdx.x; i < round; i += (int64_t)gridDim.x * kGlu) {
         const uint32_t unit = i < n ? (uint32_t)i : 0u;
         const uint32_t r = divide(unit, per);
         const int64_t c = (int64_t)(unit - r * per.d) * 16;
@@ -1460,7 +1467,7 @@ __global__ void __launch_bounds__(256, 4) swiglu_ckpt_kernel(const uint16_t *__r
 // when h is wanted, h = g s v again.  Memory bound: 8.06 bytes per element of
 // dh, 10.06 with h.
 template <bool AGAIN>
-__global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__restrict__ dh, int64_t lddh,
+__global__ void __launch_bounds__(kGlu) swiglu_ckpt_bwd_kernel(const uint16_t *__restrict__ dh, int64_t lddh,
                                                               const uint8_t *__restrict__ codes,
                                                               const uint8_t *__restrict__ sf, int64_t M, int64_t F,
                                                               UnitDiv per, const int32_t *__restrict__ n_rows,
@@ -1470,15 +1477,17 @@ __global__ void __launch_bounds__(256) swiglu_ckpt_bwd_kernel(const uint16_t *__
     grid_dependency_wait();
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * kGlu + threadIdx.x; i < n; i += (int64_t)gridDim.x * kGlu) {
         const uint32_t r = divide((uint32_t)i, per);
         const int64_t c = (int64_t)((uint32_t)i - r * per.d) * 16;
         const uint8_t *row = codes + (int64_t)r * 2 * F + c;
         uint32_t d[8], x[8], y[8], w[8];
         f32x2 g[8], v[8];
         load16(dh + r * lddh + c, d);
-        const uint4 qg = __ldg(reinterpret_cast<const uint4 *>(row)), qv = __ldg(reinterpret_cast<const uint4 *>(row + F));
-        const uint32_t sg = __ldg(sf + sf_offset(r, c >> 5, F >> 4)), sv = __ldg(sf + sf_offset(r, (c + F) >> 5, F >> 4));
+        const uint4 qg = __ldg(reinterpret_cast<const uint4 *>(row));
+        const uint4 qv = __ldg(reinterpret_cast<const uint4 *>(row + F));
+        const uint32_t sg = __ldg(sf + sf_offset(r, c >> 5, F >> 4));
+        const uint32_t sv = __ldg(sf + sf_offset(r, (c + F) >> 5, F >> 4));
         e4m3x16(qg, g);
         e4m3x16(qv, v);
         const float fg = e8m0_value(sg), fv = e8m0_value(sv);
@@ -1573,9 +1582,10 @@ struct TopkLaunch {
         const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
                            a.loss};
         return launch_dependent(
-                   kern, dim3((unsigned)topk_grid(w.nchunk, E, num_sms)), dim3(threads), smem, s, static_cast<const In *>(a.logits), a.T, E,
-                   a.ldl, (int)quads<In>(a.logits, E, a.ldl), a.mask, unit_div((uint32_t)k), (int)a.renorm, want_p, out,
-                   w.nchunk, a.ws + w.hist, reinterpret_cast<float *>(a.ws + w.psum), a.coef) != cudaSuccess;
+                   kern, dim3((unsigned)topk_grid(w.nchunk, E, num_sms)), dim3(threads), smem, s,
+                   static_cast<const In *>(a.logits), a.T, E, a.ldl, (int)quads<In>(a.logits, E, a.ldl),
+                   a.mask, unit_div((uint32_t)k), (int)a.renorm, want_p, out, w.nchunk, a.ws + w.hist,
+                   reinterpret_cast<float *>(a.ws + w.psum), a.coef) != cudaSuccess;
     }
 };
 
@@ -1587,7 +1597,8 @@ struct BwdLaunch {
     template <int LPT, int Q>
     int operator()() const {
         constexpr int per_cta = 8 * (32 / LPT);
-        const unsigned grid = (unsigned)std::min<int64_t>((a.T + per_cta - 1) / per_cta, (int64_t)num_sms * bwd_ctas<Q, NEED_P>());
+        const int64_t most = (int64_t)num_sms * bwd_ctas<Q, NEED_P>();
+        const unsigned grid = (unsigned)std::min<int64_t>((a.T + per_cta - 1) / per_cta, most);
         const bool vec = quads<In>(a.logits, a.E, a.ldl) && quads<In>(a.dlogits, a.E, a.ldd);
         return launch_dependent(route_bwd_kernel<In, LPT, Q, NEED_P>, dim3(grid), dim3(256), 0, s,
                                 static_cast<const In *>(a.logits), a.T, (int)a.E, a.ldl, (int)vec, a.topk,
@@ -1625,8 +1636,8 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
     if (small_hist(w.nchunk, E))
         return launch_dependent(route_scan_place_kernel, dim3((unsigned)w.nchunk + 1), dim3(256), 0, s, a.T,
                                 unit_div((uint32_t)a.topk), E, (int)w.nchunk,
-                                unit_div((uint32_t)hist_row(E) / 4), (const uint8_t *)(a.ws + w.hist), (const float *)psum, rows, out,
-                                a.coef) != cudaSuccess;
+                                unit_div((uint32_t)hist_row(E) / 4), (const uint8_t *)(a.ws + w.hist),
+                                (const float *)psum, rows, out, a.coef) != cudaSuccess;
     const int64_t blocks = (w.nchunk + kBlock - 1) / kBlock;
     uint16_t *prefix = reinterpret_cast<uint16_t *>(a.ws + w.prefix);
     int32_t *count = reinterpret_cast<int32_t *>(a.ws + w.count);
@@ -1655,8 +1666,11 @@ int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
 
 int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
                        int64_t T, int topk, uint16_t *out, int64_t ldo, int, cudaStream_t s) {
-    return launch_dependent(combine_kernel, dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), dim3(128), 0, s, y, R, H,
-                            ldy, rows, weights, topk, out, ldo) != cudaSuccess;
+    auto run = [&](auto kern) {
+        return launch_dependent(kern, dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), dim3(128), 0, s, y, R, H, ldy,
+                                rows, weights, topk, out, ldo) != cudaSuccess;
+    };
+    return topk <= 2 ? run(combine_kernel<2>) : run(combine_kernel<4>);  // no loads for slots that are not there
 }
 
 int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y, int64_t ldy, const uint8_t *codes,
@@ -1664,7 +1678,7 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
                            int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, int, cudaStream_t s) {
     const uint32_t slots = (uint32_t)(T * topk);
     auto run = [&](auto kern) {
-        return launch_dependent(kern, dim3((slots + 7) / 8), dim3(256), 0, s, dout, ldo, y, ldy, codes, sf, R, H, rows,
+        return launch_dependent(kern, dim3((slots + 3) / 4), dim3(128), 0, s, dout, ldo, y, ldy, codes, sf, R, H, rows,
                                 weights, slots, unit_div((uint32_t)topk), dy, lddy, dweights) != cudaSuccess;
     };
     return codes ? run(combine_bwd_kernel<true>) : run(combine_bwd_kernel<false>);
@@ -1672,20 +1686,20 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
 
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
                        int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int, cudaStream_t s) {
-    const unsigned grid = (unsigned)((M * (F / 16) + 255) / 256);
+    const unsigned grid = (unsigned)((M * (F / 16) + kGlu - 1) / kGlu);
     const UnitDiv per = unit_div((uint32_t)(F / 16));
     if (amax && launch_dependent(zero_word_kernel, dim3(1), dim3(1), 0, s, amax) != cudaSuccess) return 1;
-    return launch_dependent(swiglu_ckpt_kernel, dim3(grid), dim3(256), 0, s, u, M, F, ldu, per, n_rows, h, ldh, codes,
+    return launch_dependent(swiglu_ckpt_kernel, dim3(grid), dim3(kGlu), 0, s, u, M, F, ldu, per, n_rows, h, ldh, codes,
                             sf, amax) != cudaSuccess;
 }
 
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
                            int64_t F, const int32_t *n_rows, uint16_t *du, int64_t lddu, uint16_t *h, int64_t ldh,
                            int num_sms, cudaStream_t s) {
-    const unsigned grid = (unsigned)((M * (F / 16) + 255) / 256);
+    const unsigned grid = (unsigned)((M * (F / 16) + kGlu - 1) / kGlu);
     const UnitDiv per = unit_div((uint32_t)(F / 16));
     auto run = [&](auto kern) {
-        return launch_dependent(kern, dim3(grid), dim3(256), 0, s, dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h,
+        return launch_dependent(kern, dim3(grid), dim3(kGlu), 0, s, dh, lddh, codes, sf, M, F, per, n_rows, du, lddu, h,
                                 ldh) != cudaSuccess;
     };
     return h ? run(swiglu_ckpt_bwd_kernel<true>) : run(swiglu_ckpt_bwd_kernel<false>);

@@ -511,7 +511,7 @@ def test_offsets_past_31_bits():
     y[-4:] = torch.randn(4, H, device="cuda")
     rows = torch.tensor([[R - 1, 0], [R - 3, R - 4]], dtype=torch.int32, device="cuda")
     w = torch.rand(2, 2, device="cuda")
-    near = torch.tensor([[3, -1], [1, 0]], dtype=torch.int32, device="cuda")  # the last four rows alone (row 0 is zeros)
+    near = torch.tensor([[3, -1], [1, 0]], dtype=torch.int32, device="cuda")  # in the last four rows
     assert torch.equal(api.moe_combine(y, rows, w), api.moe_combine(y[-4:].clone(), near, w))
     g = torch.randn(2, H, device="cuda").to(torch.bfloat16)
     dy, dw = api.moe_combine_bwd(g, y, rows, w)
