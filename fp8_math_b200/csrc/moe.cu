@@ -6,6 +6,8 @@
 // gives the same bits every time.
 #include <algorithm>
 
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "moe.cuh"
 
@@ -512,20 +514,104 @@ struct RouteOut {
     float *prob_sums, *loss;
 };
 
+// The rest of the call by the CTAs of one cluster, 64 tokens each: every one adds
+// up all masks' counts, those of the CTAs before it apart, and places its slots.
+// Against a second launch: 512x128, k = 8, 7.1 us on the device instead of 8.3, and
+// a launch's host time less.
+BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, const uint16_t *sel, const float *sel_x,
+                          const float *inv, int64_t T, UnitDiv kd, int E, int ctas, int want_p, const RouteOut &out,
+                          float coef) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    __shared__ int first_token;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = (int)kd.d, rank = blockIdx.x;
+    const int t0 = rank * kChunk, here = max(0, min(kChunk, (int)T - t0)) * k;
+    int32_t *all = off + E + 1, *before = all + E + 1;
+    auto sync = [&] {
+        if (ctas > 1) cluster.sync();
+        else __syncthreads();
+    };
+    sync();  // masks and sums of all CTAs are there
+    for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+        int n = 0, b = 0;
+        for (int r = 0; r < ctas; r++) {
+            const int c = __popcll(cluster.map_shared_rank(masks, r)[e]);
+            n += c;
+            b += r < rank ? c : 0;
+        }
+        all[e] = n;
+        before[e] = b;
+    }
+    if (threadIdx.x == 0) first_token = 0;
+    __syncthreads();
+    if (warp == 0) warp_scan<false>([&](int e) { return all[e]; }, E, off);
+    __syncthreads();
+    const int total = off[E];
+    for (int i = threadIdx.x; i < here; i += blockDim.x) {
+        const int tl = (int)divide((uint32_t)i, kd);
+        const int e = (int16_t)sel[i];
+        int row = -1;
+        if (e >= 0) {
+            row = off[e] + before[e] + __popcll(masks[e] & ((1ull << tl) - 1ull));
+            out.row_index[row] = t0 + tl;
+        }
+        out.ids[t0 * k + i] = e;
+        out.weights[t0 * k + i] = sel_x[i] * inv[tl];
+        out.rows[t0 * k + i] = row;
+    }
+    if (t0 * k + here > total) {  // rows without a slot repeat the first row's token
+        for (int e = threadIdx.x; e < E; e += blockDim.x)
+            if (off[e] == 0 && off[e + 1] > 0) {  // one expert has the first row
+                int r = 0;
+                while (cluster.map_shared_rank(masks, r)[e] == 0) r++;
+                first_token = r * kChunk + __ffsll(cluster.map_shared_rank(masks, r)[e]) - 1;
+            }
+        __syncthreads();
+        for (int i = max(t0 * k, total) + threadIdx.x; i < t0 * k + here; i += blockDim.x)
+            out.row_index[i] = first_token;
+    }
+    if (rank == 0) {
+        __syncthreads();
+        float *sums = reinterpret_cast<float *>(before);
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+            out.counts[e] = all[e];
+            out.row_off[e] = off[e];
+            if (want_p && e < E) {
+                float v = 0.0f;
+                for (int r = 0; r < ctas; r++) v += cluster.map_shared_rank(red, r)[e];
+                sums[e] = v;
+                if (out.prob_sums) out.prob_sums[e] = v;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) warp_scan<true>([&](int e) { return all[e]; }, E, out.sf_row_off);
+        if (warp == 1 && out.loss) {
+            float v = 0.0f;
+            for (int e = lane; e < E; e += 32) v += (float)all[e] * sums[e];
+            v = warp_sum(v);
+            if (lane == 0) *out.loss = balance_loss(v, all[E], coef, E, k);
+        }
+    }
+    sync();  // no CTA leaves while another reads its shared memory
+}
+
 // Pass 1.  A CTA takes chunks of kChunk consecutive tokens in turn, LPT lanes a
 // token; the sums of probabilities stay in its registers.  The softmax sum runs
 // over the same registers as the choice.  The chosen experts go into one 64-bit
 // mask of tokens per expert, whose population count is the chunk's count and
 // whose bits below a token are that token's rank in the chunk: the order "by
 // expert, then token" needs no sort.  Row E of the counts is the number of tokens
-// with at least one expert.  Where the chunk is all there is, the CTA finishes
-// the call (offsets, rows, loss).  L: k <= L by sorted lists; 0: rounds for any k.
+// with at least one expert.  With `ctas` > 0 the chunks are one cluster, a CTA
+// each, which finishes the call (rows, offsets, loss) from one another's masks and
+// sums in shared memory.  L: k <= L by sorted lists; 0: rounds for any k.
 // 131072x256, k = 8: 46 of the call's 63 us, bound by instructions (235 per token;
 // minima and maxima run at half rate).
+// (The launch bound is there for the registers: 64 where a lane has few logits, so
+// that two CTAs of 512 threads share an SM, else 80.)
 template <typename In, int LPT, int Q, int L>
-__global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
+__global__ void __launch_bounds__(Q <= 2 ? 1024 : 768) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                          int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
-                                                         int renorm, int want_p, RouteOut out, int64_t nchunk,
+                                                         int renorm, int want_p, int ctas, RouteOut out, int64_t nchunk,
                                                          uint8_t *__restrict__ hist, float *__restrict__ psum,
                                                          float coef) {
     grid_dependents_launch();
@@ -536,11 +622,10 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
     float *sel_x = reinterpret_cast<float *>(words + 2 * (E + 1));     // [kChunk][k] exp(logit - top)
     float *inv = sel_x + kChunk * k;                                   // [kChunk]
     float *red = inv + kChunk;                                         // [nwarps][E] when want_p
-    int32_t *off = reinterpret_cast<int32_t *>(red + (want_p ? nwarps * E : 0));  // [E + 1] when nchunk == 1
-    uint16_t *sel = reinterpret_cast<uint16_t *>(off + (nchunk == 1 ? E + 1 : 0));     // [kChunk][k]
+    int32_t *off = reinterpret_cast<int32_t *>(red + (want_p ? nwarps * E : 0));  // 3 [E + 1] when ctas > 0
+    uint16_t *sel = reinterpret_cast<uint16_t *>(off + (ctas ? 3 * (E + 1) : 0));  // [kChunk][k]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPT;
     constexpr int kGroups = 32 / LPT;
-    const bool single = nchunk == 1;
     auto pick = [&](int tl, int j, int e, float x) {
         sel[tl * k + j] = (uint16_t)e;
         sel_x[tl * k + j] = x;
@@ -550,9 +635,9 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
     f32x2 acc[Q][2];
 #pragma unroll
     for (int q = 0; q < Q; q++) acc[q][0] = acc[q][1] = f2_pack(0.0f, 0.0f);
+    for (int i = threadIdx.x; i < 2 * (E + 1); i += blockDim.x) words[i] = 0;
+    __syncthreads();
     for (int64_t chunk = blockIdx.x; chunk < nchunk; chunk += gridDim.x) {
-        for (int i = threadIdx.x; i < 2 * (E + 1); i += blockDim.x) words[i] = 0;
-        __syncthreads();
         const int64_t t0 = chunk * kChunk;
         const int here = (int)min((int64_t)kChunk, T - t0);
         for (int w0 = warp * kGroups; w0 < here; w0 += nwarps * kGroups) {
@@ -623,30 +708,24 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
             if (in && sub == 0) inv[tl] = chosen > 0.0f ? rcp(chosen) : 0.0f;
         }
         __syncthreads();
-        if (single) {
-            if (warp == 0) warp_scan<false>([&](int e) { return __popcll(smem[e]); }, E, off);
-            __syncthreads();
-        }
+        if (ctas) break;
         for (int i = threadIdx.x; i < here * k; i += blockDim.x) {
             const int tl = (int)divide((uint32_t)i, kd);
             const int e = (int16_t)sel[i];
-            int row = e < 0 ? -1 : __popcll(smem[e] & ((1ull << tl) - 1ull));
-            if (single && e >= 0) {
-                row += off[e];
-                out.row_index[row] = tl;
-            }
             out.ids[t0 * k + i] = e;
             out.weights[t0 * k + i] = sel_x[i] * inv[tl];
-            out.rows[t0 * k + i] = row;
+            out.rows[t0 * k + i] = e < 0 ? -1 : __popcll(smem[e] & ((1ull << tl) - 1ull));
         }
-        if (!single) {
-            // a row of counts and a row of first tokens per chunk
-            uint8_t *to = hist + chunk * 2 * hist_row(E);
-            for (int e = threadIdx.x; e <= E; e += blockDim.x) {
-                const unsigned long long m = smem[e];
-                to[e] = (uint8_t)__popcll(m);
-                to[hist_row(E) + e] = (uint8_t)(m ? __ffsll(m) - 1 : 0);
-            }
+        // a row of counts and a row of first tokens per chunk
+        uint8_t *to = hist + chunk * 2 * hist_row(E);
+        for (int e = threadIdx.x; e <= E; e += blockDim.x) {
+            const unsigned long long m = smem[e];
+            to[e] = (uint8_t)__popcll(m);
+            to[hist_row(E) + e] = (uint8_t)(m ? __ffsll(m) - 1 : 0);
+        }
+        if (chunk + gridDim.x < nchunk) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < 2 * (E + 1); i += blockDim.x) words[i] = 0;
             __syncthreads();
         }
     }
@@ -667,45 +746,14 @@ __global__ void __launch_bounds__(768) route_topk_kernel(const In *__restrict__ 
         }
         __syncthreads();
     }
-    if (!single) {
-        if (want_p)
-            for (int e = threadIdx.x; e < E; e += blockDim.x) {
-                float v = 0.0f;
-                for (int w = 0; w < nwarps; w++) v += red[w * E + e];
-                psum[(int64_t)blockIdx.x * E + e] = v;
-            }
-    } else {
-        __shared__ int first_token;
-        const int slots = (int)T * k, total = off[E], tokens = __popcll(smem[E]);
-        if (threadIdx.x == 0) first_token = 0;
-        __syncthreads();
+    if (want_p)
         for (int e = threadIdx.x; e < E; e += blockDim.x) {
-            if (off[e] == 0 && off[e + 1] > 0) first_token = __ffsll(smem[e]) - 1;  // one expert has the first row
-            if (want_p) {
-                float v = 0.0f;
-                for (int w = 0; w < nwarps; w++) v += red[w * E + e];
-                red[e] = v;  // this thread's own column
-                if (out.prob_sums) out.prob_sums[e] = v;
-            }
-            out.counts[e] = off[e + 1] - off[e];
-            out.row_off[e] = off[e];
+            float v = 0.0f;
+            for (int w = 0; w < nwarps; w++) v += red[w * E + e];
+            if (ctas) red[e] = v;  // this thread's own column
+            else psum[(int64_t)blockIdx.x * E + e] = v;
         }
-        if (threadIdx.x == 0) {
-            out.counts[E] = tokens;
-            out.row_off[E] = total;
-        }
-        __syncthreads();
-        for (int i = total + threadIdx.x; i < slots; i += blockDim.x) out.row_index[i] = first_token;
-        if (warp == 0) {
-            if (out.loss) {
-                float v = 0.0f;
-                for (int e = lane; e < E; e += 32) v += (float)__popcll(smem[e]) * red[e];
-                v = warp_sum(v);
-                if (lane == 0) *out.loss = balance_loss(v, tokens, coef, E, k);
-            }
-            warp_scan<true>([&](int e) { return __popcll(smem[e]); }, E, out.sf_row_off);
-        }
-    }
+    if (ctas) finish_route(smem, red, off, sel, sel_x, inv, T, kd, E, ctas, want_p, out, coef);
 }
 
 // Pass 2, for many chunks.  A CTA takes kBlock consecutive chunks and 32 experts
@@ -1556,8 +1604,14 @@ int64_t topk_grid(int64_t nchunk, int64_t E, int num_sms) {
     return E > 128 && topk_threads(nchunk, num_sms) == 256 ? (nchunk + 1) / 2 : nchunk;
 }
 
-// Shared memory of the first pass; at most 89,608 bytes (1024 experts, 32 slots, 16 warps).
-constexpr int kRouteSmem = 96 * 1024;
+// CTAs of the cluster that takes all chunks (a power of two, eight at most: the
+// portable size), or 0: more chunks than that.
+int cluster_ctas(int64_t nchunk) {
+    return nchunk > 8 ? 0 : nchunk > 4 ? 8 : nchunk > 2 ? 4 : (int)nchunk;
+}
+
+// Shared memory of the first pass; at most 98,580 bytes (1024 experts, 32 slots, 16 warps).
+constexpr int kRouteSmem = 100 * 1024;
 
 template <typename In>
 struct TopkLaunch {
@@ -1574,18 +1628,34 @@ struct TopkLaunch {
     template <class K>
     int run(K kern) const {
         const int E = (int)a.E, k = a.topk;
-        const int threads = topk_threads(w.nchunk, num_sms);
+        const int threads = topk_threads(w.nchunk, num_sms), ctas = cluster_ctas(w.nchunk);
         const size_t smem = 8 * (size_t)(E + 1) + 4 * kChunk * (size_t)(k + 1) +
-                            (want_p ? threads / 32 * 4 * (size_t)E : 0) + (w.nchunk == 1 ? 4 * (size_t)(E + 1) : 0) +
+                            (want_p ? threads / 32 * 4 * (size_t)E : 0) + (ctas ? 12 * (size_t)(E + 1) : 0) +
                             2 * kChunk * (size_t)k;
         if (smem > 48 * 1024 && smem_attr_once(reinterpret_cast<const void *>(kern), kRouteSmem) != BSQ_OK) return 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(ctas ? ctas : topk_grid(w.nchunk, E, num_sms)));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        if (kernel_choice(BSQ_KNOB_LAUNCH_OVERLAP) != 0) {  // as launch_dependent()
+            attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+        }
+        if (ctas > 1) {
+            attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+            attr[cfg.numAttrs].val.clusterDim.x = (unsigned)ctas;
+            attr[cfg.numAttrs].val.clusterDim.y = 1;
+            attr[cfg.numAttrs++].val.clusterDim.z = 1;
+        }
+        cfg.attrs = attr;
         const RouteOut out{a.ids, a.weights, a.rows, a.row_index, a.row_off, a.sf_row_off, a.counts, a.prob_sums,
                            a.loss};
-        return launch_dependent(
-                   kern, dim3((unsigned)topk_grid(w.nchunk, E, num_sms)), dim3(threads), smem, s,
-                   static_cast<const In *>(a.logits), a.T, E, a.ldl, (int)quads<In>(a.logits, E, a.ldl),
-                   a.mask, unit_div((uint32_t)k), (int)a.renorm, want_p, out, w.nchunk, a.ws + w.hist,
-                   reinterpret_cast<float *>(a.ws + w.psum), a.coef) != cudaSuccess;
+        return cudaLaunchKernelEx(&cfg, kern, static_cast<const In *>(a.logits), a.T, E, a.ldl,
+                                  (int)quads<In>(a.logits, E, a.ldl), a.mask, unit_div((uint32_t)k), (int)a.renorm,
+                                  want_p, ctas, out, w.nchunk, a.ws + w.hist,
+                                  reinterpret_cast<float *>(a.ws + w.psum), a.coef) != cudaSuccess;
     }
 };
 
@@ -1628,7 +1698,7 @@ int launch_moe_route(const RouteArgs &a, int num_sms, cudaStream_t s) {
     if (a.bf16 ? by_experts(a.E, TopkLaunch<uint16_t>{a, w, want_p, num_sms, s})
                : by_experts(a.E, TopkLaunch<float>{a, w, want_p, num_sms, s}))
         return 1;
-    if (w.nchunk == 1) return 0;
+    if (cluster_ctas(w.nchunk)) return 0;  // done
     const int64_t rows = topk_grid(w.nchunk, a.E, num_sms);  // of sums of probabilities
     const int E = (int)a.E;
     float *psum = want_p ? reinterpret_cast<float *>(a.ws + w.psum) : nullptr;

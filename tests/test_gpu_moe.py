@@ -132,6 +132,18 @@ def test_route_of_many_tokens(T, E, k, masked):
     within(n64(r.loss), [loss], (rel + (E / 32 + 20) * U) * loss, "loss")
 
 
+@pytest.mark.parametrize("T", [64, 65, 128, 129, 256, 257, 448, 512, 513])
+@pytest.mark.parametrize("masked", [False, True])
+def test_route_around_the_cluster_sizes(T, masked):
+    """One, two, four and eight CTAs of 64 tokens that finish the call together, with CTAs that have no tokens, and
+    one token more than they take; the first CTA's tokens may all be padding."""
+    z = dev(logits_of(T, 72, T, False, "shut"))
+    mask = torch.ones(T, dtype=torch.uint8)
+    if masked:
+        mask[:min(T - 1, 70)] = 0
+    check_route(api.moe_route(z, 5, token_mask=dev(mask), balance_coef=0.3), z, 5, dev(mask), True, 0.3)
+
+
 @pytest.mark.parametrize("T,E,k", [(1, 8, 2), (130, 24, 3)])
 def test_route_of_masked_tokens_reads_nothing_of_them(T, E, k):
     """Padding may hold NaN; with every token masked nothing is routed."""
