@@ -604,8 +604,8 @@ BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, c
 // with at least one expert.  With `ctas` > 0 the chunks are one cluster, a CTA
 // each, which finishes the call (rows, offsets, loss) from one another's masks and
 // sums in shared memory.  L: k <= L by sorted lists; 0: rounds for any k.
-// 131072x256, k = 8: 46 of the call's 63 us, bound by instructions (235 per token;
-// minima and maxima run at half rate).
+// 131072x256, k = 8: three quarters of the call's 61 us, bound by instructions (235
+// per token; minima and maxima run at half rate).
 // (The launch bound is there for the registers: 64 where a lane has few logits, so
 // that two CTAs of 512 threads share an SM, else 80.)
 template <typename In, int LPT, int Q, int L>

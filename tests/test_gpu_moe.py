@@ -227,6 +227,36 @@ def test_route_bwd_difficult_logits(kind, renorm):
     check_route_bwd(z, r, torch.randn(T, k, generator=torch.Generator().manual_seed(0)), 2.0, 0.3, renorm)
 
 
+@pytest.mark.parametrize("T,E", [(40, 24), (300, 24), (5000, 24), (40000, 24), (3000, 300)])
+def test_route_loss_and_sums_each_alone(T, E):
+    """Every launch shape with the sums but no loss, and with the loss but no sums."""
+    z = dev(logits_of(T, E, T))
+    both = api.moe_route(z, 2, balance_coef=0.25)
+    sums = torch.full((E,), -1.0, device="cuda")
+    bufs = [torch.empty_like(t) for t in both[:7]]
+    r = api.moe_route(z, 2, out=(*bufs, sums, None))
+    assert torch.equal(sums, both.prob_sums) and r.loss is None
+    loss = torch.full((1,), -1.0, device="cuda")
+    r = api.moe_route(z, 2, balance_coef=0.25, out=(*bufs, None, loss))
+    assert torch.equal(loss, both.loss) and all(torch.equal(a, b) for a, b in zip(r[:7], both[:7]))
+
+
+def test_route_bwd_with_counts_of_all_ranks():
+    """Counts summed over ranks: each rank's gradient is its rows of the gradient of the loss over all tokens."""
+    T, E, k = 90, 20, 3
+    z = [dev(logits_of(T, E, s)) for s in (1, 2)]
+    whole = api.moe_route(torch.cat(z), k)
+    one = torch.ones(1, device="cuda")
+    want = api.moe_route_bwd(torch.cat(z), whole.expert_ids, whole.weights, counts=whole.counts, dloss=one,
+                             balance_coef=0.7)
+    parts = [api.moe_route(x, k) for x in z]
+    counts = parts[0].counts + parts[1].counts
+    assert torch.equal(counts, whole.counts)
+    for i, (x, r) in enumerate(zip(z, parts)):
+        d = api.moe_route_bwd(x, r.expert_ids, r.weights, counts=counts, dloss=one, balance_coef=0.7)
+        assert torch.equal(d, want[i * T:(i + 1) * T])
+
+
 def test_route_bwd_of_an_empty_slot_ignores_its_gradient():
     z = dev(logits_of(50, 8, 2, False, "shut"))
     r = api.moe_route(z, 6)
@@ -307,6 +337,12 @@ def test_combine_rows_out_of_range_add_nothing():
     assert n64(api.moe_combine(y, rows, w))[:, 0].tolist() == [2, 0, 2]
     dy, dw = api.moe_combine_bwd(torch.ones(3, 64, dtype=torch.bfloat16, device="cuda"), y, rows, w)
     assert n64(dy)[:, 0].tolist() == [2, 0, 0, 2] and n64(dw).tolist() == [[64, 0], [0, 0], [64, 0]]
+
+
+def test_combine_may_list_a_row_more_than_once():
+    y = torch.arange(1, 5, device="cuda").to(torch.bfloat16)[:, None].expand(4, 64).contiguous()
+    rows = torch.tensor([[3, 3, 3], [0, 3, 0]], dtype=torch.int32, device="cuda")
+    assert n64(api.moe_combine(y, rows))[:, 7].tolist() == [12, 6]
 
 
 def test_combine_without_tokens_or_rows():
