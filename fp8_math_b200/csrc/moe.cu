@@ -523,10 +523,9 @@ BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, c
                           float coef) {
     namespace cg = cooperative_groups;
     cg::cluster_group cluster = cg::this_cluster();
-    __shared__ int first_token;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = (int)kd.d, rank = blockIdx.x;
     const int t0 = rank * kChunk, here = max(0, min(kChunk, (int)T - t0)) * k;
-    int32_t *all = off + E + 1, *before = all + E + 1;
+    int32_t *all = off + E + 1, *before = all + E + 1, *first_token = before + E + 1;
     auto sync = [&] {
         if (ctas > 1) cluster.sync();
         else __syncthreads();
@@ -542,7 +541,7 @@ BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, c
         all[e] = n;
         before[e] = b;
     }
-    if (threadIdx.x == 0) first_token = 0;
+    if (threadIdx.x == 0) *first_token = 0;
     __syncthreads();
     if (warp == 0) warp_scan<false>([&](int e) { return all[e]; }, E, off);
     __syncthreads();
@@ -564,11 +563,11 @@ BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, c
             if (off[e] == 0 && off[e + 1] > 0) {  // one expert has the first row
                 int r = 0;
                 while (cluster.map_shared_rank(masks, r)[e] == 0) r++;
-                first_token = r * kChunk + __ffsll(cluster.map_shared_rank(masks, r)[e]) - 1;
+                *first_token = r * kChunk + __ffsll(cluster.map_shared_rank(masks, r)[e]) - 1;
             }
         __syncthreads();
         for (int i = max(t0 * k, total) + threadIdx.x; i < t0 * k + here; i += blockDim.x)
-            out.row_index[i] = first_token;
+            out.row_index[i] = *first_token;
     }
     if (rank == 0) {
         __syncthreads();
@@ -622,8 +621,8 @@ __global__ void __launch_bounds__(Q <= 2 ? 1024 : 768) route_topk_kernel(const I
     float *sel_x = reinterpret_cast<float *>(words + 2 * (E + 1));     // [kChunk][k] exp(logit - top)
     float *inv = sel_x + kChunk * k;                                   // [kChunk]
     float *red = inv + kChunk;                                         // [nwarps][E] when want_p
-    int32_t *off = reinterpret_cast<int32_t *>(red + (want_p ? nwarps * E : 0));  // 3 [E + 1] when ctas > 0
-    uint16_t *sel = reinterpret_cast<uint16_t *>(off + (ctas ? 3 * (E + 1) : 0));  // [kChunk][k]
+    int32_t *off = reinterpret_cast<int32_t *>(red + (want_p ? nwarps * E : 0));  // 3 [E + 1] + 1 when ctas > 0
+    uint16_t *sel = reinterpret_cast<uint16_t *>(off + (ctas ? 3 * (E + 1) + 1 : 0));  // [kChunk][k]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane % LPT;
     constexpr int kGroups = 32 / LPT;
     auto pick = [&](int tl, int j, int e, float x) {
@@ -1610,7 +1609,8 @@ int cluster_ctas(int64_t nchunk) {
     return nchunk > 8 ? 0 : nchunk > 4 ? 8 : nchunk > 2 ? 4 : (int)nchunk;
 }
 
-// Shared memory of the first pass; at most 98,580 bytes (1024 experts, 32 slots, 16 warps).
+// Shared memory of the first pass, all of it dynamic (a variable of static size would count towards the 48 KB that
+// need no attribute); at most 98,584 bytes (1024 experts, 32 slots, 16 warps).
 constexpr int kRouteSmem = 100 * 1024;
 
 template <typename In>
@@ -1630,7 +1630,7 @@ struct TopkLaunch {
         const int E = (int)a.E, k = a.topk;
         const int threads = topk_threads(w.nchunk, num_sms), ctas = cluster_ctas(w.nchunk);
         const size_t smem = 8 * (size_t)(E + 1) + 4 * kChunk * (size_t)(k + 1) +
-                            (want_p ? threads / 32 * 4 * (size_t)E : 0) + (ctas ? 12 * (size_t)(E + 1) : 0) +
+                            (want_p ? threads / 32 * 4 * (size_t)E : 0) + (ctas ? 12 * (size_t)(E + 1) + 4 : 0) +
                             2 * kChunk * (size_t)k;
         if (smem > 48 * 1024 && smem_attr_once(reinterpret_cast<const void *>(kern), kRouteSmem) != BSQ_OK) return 1;
         cudaLaunchConfig_t cfg = {};

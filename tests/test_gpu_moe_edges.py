@@ -1,0 +1,51 @@
+"""The mixture-of-experts training operators where their kernels change form:
+sizes at the limit of shared memory, more slots than lanes, tokens of a second
+round, several chunks per CTA, sigmoids below the normal numbers, exponents far
+below the largest; and refusals with their exact status.  Tolerances count fp32
+roundings as in test_gpu_moe.py."""
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+import torch
+
+import moe_ref as ref
+from fp8_math_b200 import api, bsq
+from gpu_util import dev
+from moe_ref import B, U, within
+from test_gpu_moe import check_route_bwd, decode8, ints, logits_of, n64
+
+pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+# (T, E, k) whose first launch asks for 48 KB of dynamic shared memory, or up to 15 bytes less: one CTA of a cluster,
+# 16 warps, 8 warps
+AT_48K = [(65, 440, 31), (65, 463, 26), (65, 472, 24), (65, 495, 19), (65, 504, 17), (65, 527, 12), (65, 536, 10),
+          (65, 559, 5), (65, 568, 3), (1000, 519, 30), (1000, 535, 27), (1000, 551, 24), (1000, 567, 21),
+          (1000, 583, 18), (1000, 599, 15), (1000, 615, 12), (1000, 631, 9), (1000, 647, 6), (1000, 663, 3),
+          (20000, 915, 32), (20000, 934, 30), (20000, 963, 27), (20000, 982, 25), (20000, 1011, 22)]
+
+
+def route_at_48k():
+    """Run in a process of its own: a call of a larger size would raise the limit for the kernel it takes."""
+    for T, E, k in AT_48K:
+        for dtype in (torch.float32, torch.bfloat16):
+            z = torch.randn(T, E, device="cuda", generator=torch.Generator("cuda").manual_seed(E)).to(dtype)
+            r = api.moe_route(z, k, balance_coef=0.5)
+            best = torch.sort(z.double(), dim=1, descending=True, stable=True)
+            assert torch.equal(r.expert_ids.long(), best.indices[:, :k]), (T, E, k)
+            w = torch.softmax(best.values[:, :k], 1)
+            assert (r.weights.double() - w).abs().max() < 1e-5, (T, E, k)
+            assert (r.prob_sums.double() - torch.softmax(z.double(), 1).sum(0)).abs().max() < 1e-5 * T, (T, E, k)
+    assert bsq.bsq_check() == bsq.BSQ_OK
+    print("route_at_48k ok")
+
+
+def test_route_at_the_default_limit_of_shared_memory():
+    code = f"import sys; sys.path[:0] = [{os.path.dirname(HERE)!r}, {HERE!r}]; import test_gpu_moe_edges as m; " \
+           "m.route_at_48k()"
+    p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and "route_at_48k ok" in p.stdout, p.stderr[-2000:]
