@@ -585,10 +585,10 @@ int bsq_moe_route(const void *logits, int logits_type, int64_t T, int64_t E, int
                   int topk, int renorm, int32_t *ids, float *weights, int32_t *rows, int32_t *row_index,
                   int32_t *row_off, int32_t *sf_row_off, int32_t *counts, float *prob_sums, float balance_coef,
                   float *loss, void *workspace, size_t workspace_bytes, void *stream) {
-    if ((logits_type != BSQ_OUT_F32 && logits_type != BSQ_OUT_BF16) || !row_off || !sf_row_off || !counts ||
-        !workspace || ldl < E)
-        return BSQ_ERR_INVALID;
+    if ((logits_type != BSQ_OUT_F32 && logits_type != BSQ_OUT_BF16) || ldl < E) return BSQ_ERR_INVALID;
+    // before the pointers: the workspace of a size that is not supported is empty, and may be a null pointer
     if (int st = route_sizes(T, E, topk)) return st;
+    if (!row_off || !sf_row_off || !counts || !workspace) return BSQ_ERR_INVALID;
     if (T > 0 && (!logits || !ids || !weights || !rows || !row_index)) return BSQ_ERR_INVALID;
     if (workspace_bytes < bsq_moe_route_workspace(T, E)) return BSQ_ERR_INVALID;
     if ((reinterpret_cast<uintptr_t>(logits) & (logits_type == BSQ_OUT_F32 ? 3u : 1u)) || !aligned4(ids) ||

@@ -49,3 +49,16 @@ def test_route_at_the_default_limit_of_shared_memory():
            "m.route_at_48k()"
     p = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert p.returncode == 0 and "route_at_48k ok" in p.stdout, p.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ refusals
+def status_of(call):
+    with pytest.raises(bsq.BsqError) as e:
+        call()
+    return e.value.status
+
+
+def test_route_says_unsupported_for_sizes_it_does_not_take():
+    assert status_of(lambda: api.moe_route(torch.zeros(4, 1025, device="cuda"), 2)) == bsq.BSQ_ERR_UNSUPPORTED
+    assert status_of(lambda: api.moe_route(torch.zeros(4, 64, device="cuda"), 33)) == bsq.BSQ_ERR_UNSUPPORTED
+    assert status_of(lambda: api.moe_route(torch.zeros(4, 8, device="cuda"), 9)) == bsq.BSQ_ERR_INVALID

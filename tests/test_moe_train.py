@@ -164,3 +164,18 @@ def test_swiglu_refusals(L):
     for bad in [dict(dh=264), dict(c=264), dict(s=264), dict(du=264), dict(h=264, ldh=32), dict(h=p, ldh=36),
                 dict(lddh=36), dict(lddu=68), dict(n=258)]:
         assert bwd(**bad) == L.BSQ_ERR_ALIGN, bad
+
+
+def test_route_sizes_are_told_before_the_workspace_is_asked_for(L):
+    """For sizes that are not supported the workspace has 0 bytes, and so a caller's pointer may be null."""
+    lib, p = L.lib(), 256
+
+    def call(T=16, E=8, k=2, ldl=2048):
+        n = L.bsq_moe_route_workspace(T, E)
+        return lib.bsq_moe_route(p, 0, T, E, ldl, None, k, 1, p, p, p, p, p, p, p, None, 0.0, None, p if n else None, n,
+                                 None)
+
+    assert call(E=1025) == L.BSQ_ERR_UNSUPPORTED
+    assert call(T=1 << 31) == L.BSQ_ERR_UNSUPPORTED
+    assert call(T=(1 << 31) - 1024, E=1024) == L.BSQ_ERR_UNSUPPORTED
+    assert call(E=0) == L.BSQ_ERR_INVALID and call(T=-1) == L.BSQ_ERR_INVALID
