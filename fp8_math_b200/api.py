@@ -318,10 +318,11 @@ def moe_route(logits, topk, token_mask=None, renorm=True, balance_coef=None, out
     return out
 
 
-def moe_route_bwd(logits, expert_ids, weights, dweights=None, counts=None, dloss=None, balance_coef=0.0, renorm=True,
+def moe_route_bwd(logits, expert_ids, weights, dweights=None, counts=None, dloss=None, balance_coef=None, renorm=True,
                   out=None):
     """Gradient of the logits from the weights' gradient (fp32 [T, k]) and the
-    balance loss's (fp32 [1], with the router's counts and its balance_coef)."""
+    balance loss's (fp32 [1]; it takes the router's counts and balance_coef,
+    and is refused without them)."""
     fn = "moe_route_bwd"
     dev = torch.cuda.current_device()
     dtype = logits.dtype
@@ -339,11 +340,14 @@ def moe_route_bwd(logits, expert_ids, weights, dweights=None, counts=None, dloss
         _arr(fn, counts, torch.int32, E + 1, dev)
     if dloss is not None:
         _arr(fn, dloss, torch.float32, 1, dev)
+        if balance_coef is None:
+            _refuse(fn)
     if out is None:
         out = torch.empty(T, E, dtype=dtype, device=logits.device)
     ldd = _mat(fn, out, dtype, T, E, dev)
     bsq.bsq_moe_route_bwd(logits, bsq.BSQ_OUT_F32 if dtype is torch.float32 else bsq.BSQ_OUT_BF16, T, E, ld, k, renorm,
-                          expert_ids, weights, dweights, counts, balance_coef, dloss, out, ldd)
+                          expert_ids, weights, dweights, counts, 0.0 if balance_coef is None else balance_coef, dloss,
+                          out, ldd)
     return out
 
 

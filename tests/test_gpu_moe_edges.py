@@ -62,3 +62,14 @@ def test_route_says_unsupported_for_sizes_it_does_not_take():
     assert status_of(lambda: api.moe_route(torch.zeros(4, 1025, device="cuda"), 2)) == bsq.BSQ_ERR_UNSUPPORTED
     assert status_of(lambda: api.moe_route(torch.zeros(4, 64, device="cuda"), 33)) == bsq.BSQ_ERR_UNSUPPORTED
     assert status_of(lambda: api.moe_route(torch.zeros(4, 8, device="cuda"), 9)) == bsq.BSQ_ERR_INVALID
+
+
+def test_route_bwd_refuses_a_loss_gradient_without_its_coefficient():
+    z = dev(logits_of(20, 8, 1))
+    r = api.moe_route(z, 2, balance_coef=0.5)
+    one = torch.ones(1, device="cuda")
+    assert status_of(lambda: api.moe_route_bwd(z, r.expert_ids, r.weights, counts=r.counts, dloss=one)) == \
+        bsq.BSQ_ERR_INVALID
+    with_loss = api.moe_route_bwd(z, r.expert_ids, r.weights, counts=r.counts, dloss=one, balance_coef=0.5)
+    assert (with_loss != 0).any()
+    assert (api.moe_route_bwd(z, r.expert_ids, r.weights, counts=r.counts, dloss=one, balance_coef=0.0) == 0).all()
