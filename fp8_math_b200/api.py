@@ -305,8 +305,8 @@ def moe_route(logits, topk, token_mask=None, renorm=True, balance_coef=None, out
             _arr(fn, prob_sums, torch.float32, E, dev)
         if loss is not None:
             _arr(fn, loss, torch.float32, 1, dev)
-            if not with_loss:
-                _refuse(fn)
+        if (loss is not None) != with_loss:  # a coefficient and a place for the loss come together
+            _refuse(fn)
     if token_mask is not None:
         _arr(fn, token_mask, torch.bool if token_mask.dtype is torch.bool else torch.uint8, T, dev)
     if workspace is None:

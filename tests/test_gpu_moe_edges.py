@@ -73,3 +73,11 @@ def test_route_bwd_refuses_a_loss_gradient_without_its_coefficient():
     with_loss = api.moe_route_bwd(z, r.expert_ids, r.weights, counts=r.counts, dloss=one, balance_coef=0.5)
     assert (with_loss != 0).any()
     assert (api.moe_route_bwd(z, r.expert_ids, r.weights, counts=r.counts, dloss=one, balance_coef=0.0) == 0).all()
+
+
+def test_route_refuses_a_coefficient_without_a_place_for_the_loss():
+    z = dev(logits_of(20, 8, 1))
+    r = api.moe_route(z, 2, balance_coef=0.5)
+    for out in [(*r[:7], r.prob_sums, None), (*r[:7], None, None)]:
+        assert status_of(lambda: api.moe_route(z, 2, balance_coef=0.5, out=out)) == bsq.BSQ_ERR_INVALID
+    assert api.moe_route(z, 2, out=(*r[:7], None, None)).loss is None
