@@ -415,7 +415,8 @@ def _scales(fn, sf, rows, nblocks, dev):
 def swiglu_ckpt(u, n_rows=None, amax=True, out=None):
     """h = silu(gate) * v of u [M, 2F] = (gate | v) in bf16, and u in MXFP8 for
     the backward pass: (h [M, F] bf16, codes [M, 2F], sf swizzled, amax [1] of
-    h or None).  n_rows int32 [1]: only that many rows exist."""
+    h or None).  n_rows int32 [1]: only that many rows exist; without out, the
+    others are zeros."""
     fn = "swiglu_ckpt"
     dev = torch.cuda.current_device()
     if u.dim() != 2 or u.shape[1] % 2:
@@ -423,8 +424,9 @@ def swiglu_ckpt(u, n_rows=None, amax=True, out=None):
     M, F = u.shape[0], u.shape[1] // 2
     ldu = _mat(fn, u, torch.bfloat16, M, 2 * F, dev)
     if out is None:
-        out = (torch.empty(M, F, dtype=torch.bfloat16, device=u.device),
-               torch.empty(M, 2 * F, dtype=torch.uint8, device=u.device),
+        make = torch.empty if n_rows is None else torch.zeros
+        out = (make(M, F, dtype=torch.bfloat16, device=u.device),
+               make(M, 2 * F, dtype=torch.uint8, device=u.device),
                torch.zeros(sf_bytes(M, F // 16), dtype=torch.uint8, device=u.device),
                torch.empty(1, dtype=torch.float32, device=u.device) if amax else None)
     h, codes, sf, am = out
@@ -441,7 +443,8 @@ def swiglu_ckpt(u, n_rows=None, amax=True, out=None):
 
 def swiglu_ckpt_bwd(dh, codes, sf, n_rows=None, recompute_h=False, out=None):
     """Gradient of swiglu_ckpt's u from dh [M, F] (bf16) and the checkpoint:
-    (du [M, 2F] bf16, h [M, F] bf16 formed again from the checkpoint, or None)."""
+    (du [M, 2F] bf16, h [M, F] bf16 formed again from the checkpoint, or None).
+    n_rows as in swiglu_ckpt."""
     fn = "swiglu_ckpt_bwd"
     dev = torch.cuda.current_device()
     if dh.dim() != 2:
@@ -453,8 +456,9 @@ def swiglu_ckpt_bwd(dh, codes, sf, n_rows=None, recompute_h=False, out=None):
     if n_rows is not None:
         _arr(fn, n_rows, torch.int32, 1, dev)
     if out is None:
-        out = (torch.empty(M, 2 * F, dtype=torch.bfloat16, device=dh.device),
-               torch.empty(M, F, dtype=torch.bfloat16, device=dh.device) if recompute_h else None)
+        make = torch.empty if n_rows is None else torch.zeros
+        out = (make(M, 2 * F, dtype=torch.bfloat16, device=dh.device),
+               make(M, F, dtype=torch.bfloat16, device=dh.device) if recompute_h else None)
     du, h = out
     lddu = _mat(fn, du, torch.bfloat16, M, 2 * F, dev)
     ldh = _mat(fn, h, torch.bfloat16, M, F, dev) if h is not None else 0

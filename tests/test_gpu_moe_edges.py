@@ -81,3 +81,22 @@ def test_route_refuses_a_coefficient_without_a_place_for_the_loss():
     for out in [(*r[:7], r.prob_sums, None), (*r[:7], None, None)]:
         assert status_of(lambda: api.moe_route(z, 2, balance_coef=0.5, out=out)) == bsq.BSQ_ERR_INVALID
     assert api.moe_route(z, 2, out=(*r[:7], None, None)).loss is None
+
+
+@pytest.mark.parametrize("n", [0, 3, 40])
+def test_swiglu_rows_that_do_not_exist_are_zeros_without_out(n):
+    """A buffer that the wrapper makes has no row left unwritten: whole-tensor calls read it next."""
+    M, F = 40, 64
+    u = torch.randn(M, 2 * F, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    count = torch.tensor([n], dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        for size in (M * F * 2, M * F, M * F * 4):  # what the allocator hands out next holds NaN and large codes
+            junk = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+            del junk
+        h, codes, sf, _ = api.swiglu_ckpt(u, n_rows=count)
+        assert (h[n:].view(torch.int16) == 0).all() and (codes[n:] == 0).all()
+        for size in (M * F * 2, M * F * 4):
+            junk = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+            del junk
+        du, again = api.swiglu_ckpt_bwd(h, codes, sf, n_rows=count, recompute_h=True)
+        assert (du[n:].view(torch.int16) == 0).all() and (again[n:].view(torch.int16) == 0).all()
