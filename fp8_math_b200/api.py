@@ -238,13 +238,14 @@ def _refuse(fn):
 
 def _arr(fn, t, dtype, n, dev):
     """t is a contiguous tensor of n elements of this type on device dev (the current one)."""
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or t.get_device() != dev:
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.numel() != n or not t.is_contiguous() or
+            t.get_device() != dev):
         _refuse(fn)
 
 
 def _mat(fn, t, dtype, rows, cols, dev):
     """t is a row-major [rows, cols] matrix; returns its leading dimension."""
-    if t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != (rows, cols) or t.get_device() != dev:
         _refuse(fn)
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
@@ -278,7 +279,7 @@ def moe_route(logits, topk, token_mask=None, renorm=True, balance_coef=None, out
     fn = "moe_route"
     dev = torch.cuda.current_device()
     dtype = logits.dtype
-    if logits.dim() != 2 or (dtype is not torch.float32 and dtype is not torch.bfloat16):
+    if logits.dim() != 2 or (dtype is not torch.float32 and dtype is not torch.bfloat16) or topk < 1:
         _refuse(fn)
     T, E = logits.shape
     ld = _mat(fn, logits, dtype, T, E, dev)
@@ -407,6 +408,8 @@ def moe_combine_bwd(dout, y, rows, weights, out=None):
 
 def _scales(fn, sf, rows, nblocks, dev):
     """sf is a swizzled scale-factor buffer for at least this many rows."""
+    if not isinstance(sf, torch.Tensor):
+        _refuse(fn)
     _arr(fn, sf, torch.uint8, sf.numel(), dev)
     if sf.numel() < -(-rows // 128) * 128 * (-(-nblocks // 4) * 4):
         _refuse(fn)

@@ -83,6 +83,24 @@ def test_route_refuses_a_coefficient_without_a_place_for_the_loss():
     assert api.moe_route(z, 2, out=(*r[:7], None, None)).loss is None
 
 
+def test_wrappers_refuse_with_the_librarys_error():
+    """Each of these is a BsqError of status invalid, never an error of another kind from inside the wrapper."""
+    z = torch.zeros(4, 8, device="cuda")
+    i = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    w = torch.zeros(4, 2, device="cuda")
+    y = torch.zeros(8, 64, dtype=torch.bfloat16, device="cuda")
+    c = torch.zeros(8, 64, dtype=torch.uint8, device="cuda")
+    d = torch.zeros(4, 64, dtype=torch.bfloat16, device="cuda")
+    s = torch.zeros(api.sf_bytes(8, 2), dtype=torch.uint8, device="cuda")
+    for bad in [lambda: api.moe_route(z, 0), lambda: api.moe_route(z, -1), lambda: api.moe_route_bwd(z, i, None),
+                lambda: api.moe_combine_bwd(d, y, i, None), lambda: api.moe_combine_bwd(None, y, i, w),
+                lambda: api.moe_combine_bwd(d, (c, None), i, w), lambda: api.swiglu_ckpt_bwd(y[:, :32], None, s),
+                lambda: api.swiglu_ckpt_bwd(y[:, :32], c, None),
+                lambda: api.moe_combine(y, i, out=[1.0]), lambda: api.moe_combine(y, i, [1.0] * 8),
+                lambda: api.swiglu_ckpt(y, n_rows=8)]:
+        assert status_of(bad) == bsq.BSQ_ERR_INVALID
+
+
 @pytest.mark.parametrize("n", [0, 3, 40])
 def test_swiglu_rows_that_do_not_exist_are_zeros_without_out(n):
     """A buffer that the wrapper makes has no row left unwritten: whole-tensor calls read it next."""
