@@ -1402,16 +1402,18 @@ __global__ void __launch_bounds__(128) combine_bwd_kernel(const uint16_t *__rest
 }
 
 // ------------------------------------------------------------------ gated SiLU with an MXFP8 checkpoint
-// sigmoid of a pair, 1 / (1 + 2^(-g log2 e)).  Relative error (9 + 2 |g|) 2^-24
-// at most, the |g| from the rounding of the exponent; results are rounded to
-// 2^-8.  2^x overflows to infinity, whose reciprocal is 0: a sigmoid below 2^-126
-// (g < -87.3) is 0.  (Keeping its subnormal values takes a branch-free form with
-// exp(-|g|) and a select, 3.5 instructions of 26 a value more.)
-BSQ_DEV f32x2 sigmoid2(f32x2 g) {
+// sigmoid of a pair and g times it, through q = 2^(g log2 e / 2) with the exponent held at 32 (g = 44, where the
+// sigmoid is 1 to 2^-63): s = q r, g s = (g r) q with r = q / (1 + q^2).  No factor leaves the normal numbers before
+// the last product does, so s is right below 2^-126 (g < -87.3) too.  Relative error (13 + 2 |g|) 2^-24 at most, the
+// |g| from the rounding of the exponent, and one step more for g s; results are rounded to 2^-8.
+BSQ_DEV f32x2 sigmoid2(f32x2 g, f32x2 &gs) {
     float a, b;
-    f2_unpack(f2_mul(g, f2_pack(-kLog2e, -kLog2e)), a, b);
-    f2_unpack(f2_add(f2_pack(ex2(a), ex2(b)), f2_pack(1.0f, 1.0f)), a, b);
-    return f2_pack(rcp(a), rcp(b));
+    f2_unpack(f2_mul(g, f2_pack(0.5f * kLog2e, 0.5f * kLog2e)), a, b);
+    const f32x2 q = f2_pack(ex2(fminf(a, 32.0f)), ex2(fminf(b, 32.0f)));
+    f2_unpack(f2_fma(q, q, f2_pack(1.0f, 1.0f)), a, b);
+    const f32x2 r = f2_mul(q, f2_pack(rcp(a), rcp(b)));
+    gs = f2_mul(f2_mul(g, r), q);
+    return f2_mul(q, r);
 }
 
 // Larger of two bf16 pairs of magnitudes, lane by lane.
@@ -1491,8 +1493,10 @@ __global__ void __launch_bounds__(kGlu, 1024 / kGlu)
 #pragma unroll
         for (int q = 0; q < 8; q++) {
             const f32x2 gq = f2_pack(bf16_lo(g[q]), bf16_hi(g[q]));
+            f32x2 gs;
+            sigmoid2(gq, gs);
             float a, b;
-            f2_unpack(f2_mul(f2_mul(gq, sigmoid2(gq)), f2_pack(bf16_lo(v[q]), bf16_hi(v[q]))), a, b);
+            f2_unpack(f2_mul(gs, f2_pack(bf16_lo(v[q]), bf16_hi(v[q]))), a, b);
             o[q] = pack_bf16(a, b);
             top = max_bf16x2(top, o[q] & kAbs2);
         }
@@ -1546,7 +1550,8 @@ __global__ void __launch_bounds__(kGlu) swiglu_ckpt_bwd_kernel(const uint16_t *_
         }
 #pragma unroll
         for (int q = 0; q < 8; q++) {
-            const f32x2 dd = f2_pack(bf16_lo(d[q]), bf16_hi(d[q])), sg2 = sigmoid2(g[q]), gs = f2_mul(g[q], sg2);
+            f32x2 gs;
+            const f32x2 dd = f2_pack(bf16_lo(d[q]), bf16_hi(d[q])), sg2 = sigmoid2(g[q], gs);
             float a, b;
             f2_unpack(f2_mul(dd, gs), a, b);
             y[q] = pack_bf16(a, b);

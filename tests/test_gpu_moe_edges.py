@@ -118,3 +118,41 @@ def test_swiglu_rows_that_do_not_exist_are_zeros_without_out(n):
             del junk
         du, again = api.swiglu_ckpt_bwd(h, codes, sf, n_rows=count, recompute_h=True)
         assert (du[n:].view(torch.int16) == 0).all() and (again[n:].view(torch.int16) == 0).all()
+
+
+# ------------------------------------------------------------------ gated SiLU
+def far_gates(M, F, seed):
+    """Gates between -150 and -80 with v up to 1e32, so that h is an ordinary number though the sigmoid is not."""
+    g = torch.Generator().manual_seed(seed)
+    u = torch.empty(M, 2 * F)
+    u[:, :F] = -80 - 70 * torch.rand(M, F, generator=g) ** 2
+    u[:, F:] = 10.0 ** (32 * torch.rand(M, F, generator=g)) * torch.randn(M, F, generator=g)
+    return u.to(torch.bfloat16)
+
+
+def test_swiglu_keeps_sigmoids_below_the_normal_numbers():
+    """The sigmoid: 2 |g| for the square of a half exponent, 2 x 4 for ex2, four products and sums, the reciprocal 2;
+    one more product with v; bf16's rounding.  g s and s are held in fp32 with its subnormal numbers: half a step of
+    those (2^-150) times v; bf16's own half step there is 2^-134."""
+    M, F = 64, 512
+    u = far_gates(M, F, 1)
+    h, codes, sf, _ = api.swiglu_ckpt(dev(u))
+    g, v = n64(u)[:, :F], n64(u)[:, F:]
+    want = ref.swiglu(n64(u))
+    assert (abs(want) > 1e-30).mean() > 0.1
+    tol = (2 * abs(g) + 8 + 4 + 2 + 1) * U
+    within(n64(h), want, (B + tol) * abs(want) + 2.0 ** -149 * abs(v) + 2.0 ** -134, "h")
+    # the gradient, on the decoded values
+    dh = torch.randn(M, F, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    du, again = api.swiglu_ckpt_bwd(dev(dh), codes, sf, recompute_h=True)
+    x = decode8(codes, sf)
+    g, v = x[:, :F], x[:, F:]
+    want = ref.swiglu(x)
+    tol = (2 * abs(g) + 15) * U
+    within(n64(again), want, (B + tol) * abs(want) + 2.0 ** -149 * abs(v) + 2.0 ** -134, "h again")
+    want, mag = ref.swiglu_bwd(n64(dh), x)
+    d = abs(n64(dh))
+    assert (abs(want[:, :F]) > 1e-30).mean() > 0.1
+    sub = 2.0 ** -148 * np.concatenate([d * abs(v), d], 1)  # s and g s, each half a step
+    t = np.concatenate([tol, tol], 1) + 6 * U
+    within(n64(du), want, t * mag + sub + B * (abs(want) + sub) + 2.0 ** -134, "du")
