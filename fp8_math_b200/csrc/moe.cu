@@ -164,14 +164,35 @@ struct Row<float, LPT, Q> {
     }
 };
 
-// exp(x[i] - top), through 2^x; -inf gives 0.
+// max(a, b), NaN when one of them is NaN
+BSQ_DEV float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// e^d = 2^t (1 + (d - t ln 2)) with t = fl(d log2 e): the second factor takes
+// back the roundings of t and of log2 e, which alone would be |d| 2^-23 (ln 2 in
+// fp32 leaves |d| 2^-28).  d is held at -150, where 2^t is 0: a logit of -inf,
+// or one so low that the difference overflows, would give a factor of NaN.
+constexpr float kLn2 = 0.693147180559945309f, kLowest = -150.0f;
+
+BSQ_DEV float exp_of(float d) {
+    d = max_nan(d, kLowest);
+    const float t = d * kLog2e, p = ex2(t);
+    return fmaf(p, fmaf(t, -kLn2, d), p);
+}
+// exp(x[i] - top); -inf gives 0.
 BSQ_DEV void exp_below4(float x[4], f32x2 top2) {
-    const f32x2 l2 = f2_pack(kLog2e, kLog2e);
+    const f32x2 l2 = f2_pack(kLog2e, kLog2e), ln2 = f2_pack(-kLn2, -kLn2);
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
-        f2_unpack(f2_mul(f2_sub(f2_pack(x[i], x[i + 1]), top2), l2), x[i], x[i + 1]);
-        x[i] = ex2(x[i]);
-        x[i + 1] = ex2(x[i + 1]);
+        float a, b;
+        f2_unpack(f2_sub(f2_pack(x[i], x[i + 1]), top2), a, b);
+        const f32x2 d = f2_pack(max_nan(a, kLowest), max_nan(b, kLowest)), t = f2_mul(d, l2);
+        f2_unpack(t, a, b);
+        const f32x2 p = f2_pack(ex2(a), ex2(b));
+        f2_unpack(f2_fma(p, f2_fma(t, ln2, d), p), x[i], x[i + 1]);
     }
 }
 
@@ -653,7 +674,7 @@ __global__ void __launch_bounds__(Q <= 2 ? 1024 : 768) route_topk_kernel(const I
                 done = choose<L == 0 ? 4 : L>(row, logits + (t0 + tl) * ldl, sub, E, vec, k, e, z);
                 if (done) {  // the same for the whole warp
                     top = __shfl_sync(kFull, e >= 0 ? z : 0.0f, lane & ~(LPT - 1));
-                    const float x = e >= 0 ? ex2((z - top) * kLog2e) : 0.0f;
+                    const float x = e >= 0 ? exp_of(z - top) : 0.0f;
                     chosen = group_sum<LPT>(x);
                     if (in && sub < k) pick(tl, sub, e, x);
                 }
@@ -669,7 +690,7 @@ __global__ void __launch_bounds__(Q <= 2 ? 1024 : 768) route_topk_kernel(const I
                         const float z = c.pop(row, sub, e);
                         const bool ok = z > -INFINITY;
                         if (j == 0 && ok) top = z;
-                        const float x = ok ? ex2((z - top) * kLog2e) : 0.0f;
+                        const float x = ok ? exp_of(z - top) : 0.0f;
                         chosen += x;
                         if (ok && sub == j - j0) {
                             my_e = e;

@@ -120,6 +120,36 @@ def test_swiglu_rows_that_do_not_exist_are_zeros_without_out(n):
         assert (du[n:].view(torch.int16) == 0).all() and (again[n:].view(torch.int16) == 0).all()
 
 
+def exact_differences(T, E, seed):
+    """fp32 logits whose differences from the largest are exact (multiples of 1/64 below 64 in magnitude), far apart:
+    the weights' exponentials then have no rounding that grows with the distance."""
+    z = torch.randint(-84 * 64, 1, (T, E), generator=torch.Generator().manual_seed(seed)).float() / 64
+    z[:, 0] = 0
+    return z
+
+
+@pytest.mark.parametrize("E,k", [(8, 8), (12, 12), (5, 4), (200, 8)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_exponentials_far_below_the_largest(E, k, renorm):
+    """e^d for an exact d: 0.05 |d| U from the constant that splits d, ex2 4 U, its correction 1 U; then the sum over E
+    (a lane's quads, 5 exchanges), the reciprocal 2 U and two products."""
+    T = 2000
+    z = exact_differences(T, E, E)
+    r = api.moe_route(dev(z), k, renorm=renorm, balance_coef=1.0)
+    ids = np.argsort(-n64(z), axis=1, kind="stable")[:, :k]
+    assert np.array_equal(ints(r.expert_ids), ids)
+    x = np.exp(n64(z))
+    chosen = np.take_along_axis(x, ids, 1)
+    w = chosen / (chosen if renorm else x).sum(1, keepdims=True)
+    rel = 2 * (0.05 * 84 + 5) + -(-E // 32) + 5 + 2 + 2
+    within(n64(r.weights), w, rel * U * w, "weights")
+    # gradient of the loss alone: p, the bias's sum, their difference and product
+    one = torch.ones(1, device="cuda")
+    d = api.moe_route_bwd(dev(z), r.expert_ids, r.weights, counts=r.counts, dloss=one, balance_coef=1.0, renorm=renorm)
+    want, mag = ref.route_bwd(n64(z), ids, n64(r.weights), None, ints(r.counts), 1.0, 1.0, renorm)
+    within(n64(d), want, (2 * rel + 10) * U * mag + 1e-37, "dlogits")
+
+
 # ------------------------------------------------------------------ gated SiLU
 def far_gates(M, F, seed):
     """Gates between -150 and -80 with v up to 1e32, so that h is an ordinary number though the sigmoid is not."""
