@@ -146,3 +146,78 @@ def test_gemm_writes_only_its_tile_of_c(fmt, M, N, K, out_bf16):
     assert np.isnan(h[0]).all() and np.isnan(h[M + 1]).all(), "rows around C written"
     assert np.isnan(h[1:M + 1, N:]).all(), "columns past N written"
     assert np.isfinite(h[1:M + 1, :N]).all(), "C not fully written"
+
+
+def guarded_as(dtype, *shape):
+    """(whole buffer, its bytes, a view of this type and shape in its middle)."""
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    buf, view = guarded(n)
+    return buf, n, view.view(dtype).view(*shape)
+
+
+@pytest.mark.parametrize("T,E,k,bf16", [(1, 3, 2, False), (70, 72, 5, False), (500, 20, 3, True), (700, 33, 8, True),
+                                        (9000, 257, 2, False), (20001, 160, 9, True)])
+def test_moe_route_writes_only_its_outputs(T, E, k, bf16):
+    """Every launch shape, some tokens masked, so that row_index ends in rows without a slot."""
+    g = torch.Generator().manual_seed(T)
+    z = dev(torch.randn(T, E, generator=g).to(torch.bfloat16 if bf16 else torch.float32))
+    mask = dev((torch.rand(T, generator=g) < 0.7).to(torch.uint8))
+    i32, f32 = torch.int32, torch.float32
+    kinds = [(i32, T, k), (f32, T, k), (i32, T, k), (i32, T * k), (i32, E + 1), (i32, E + 1), (i32, E + 1), (f32, E),
+             (f32, 1)]
+    bufs = [guarded_as(*kind) for kind in kinds]
+    nb = api.moe_route_workspace(T, E)
+    wb, ws = guarded(nb)
+    r = api.moe_route(z, k, token_mask=mask, balance_coef=0.1, out=[b[2] for b in bufs], workspace=ws)
+    db, dn, d = guarded_as(z.dtype, T, E)
+    api.moe_route_bwd(z, r.expert_ids, r.weights, dweights=torch.rand_like(r.weights), counts=r.counts, dloss=r.loss,
+                      balance_coef=0.1, out=d)
+    assert bsq.bsq_check() == bsq.BSQ_OK
+    for (buf, n, _), name in zip(bufs, r._fields):
+        check_guards(buf, n, name)
+    check_guards(wb, nb, "workspace")
+    check_guards(db, dn, "dlogits")
+
+
+@pytest.mark.parametrize("T,k,H", [(1, 1, 8), (37, 6, 1000), (20, 3, 2080), (5, 2, 4104)])
+@pytest.mark.parametrize("y8", [False, True])
+def test_moe_combine_writes_only_its_outputs(T, k, H, y8):
+    if y8:
+        H = -(-H // 32) * 32
+    R = T * k
+    y = dev(edge(R, H, T + H))
+    rows = dev(torch.randperm(R, generator=torch.Generator().manual_seed(1)).view(T, k).to(torch.int32))
+    w = torch.rand(T, k, device="cuda")
+    ob, on, out = guarded_as(torch.bfloat16, T, H)
+    api.moe_combine(y, rows, w, out=out)
+    yb, yn, dy = guarded_as(torch.bfloat16, R, H)
+    wb, wn, dw = guarded_as(torch.float32, T, k)
+    api.moe_combine_bwd(out, api.quant_mxfp8(y) if y8 else y, rows, w, out=(dy, dw))
+    assert bsq.bsq_check() == bsq.BSQ_OK
+    check_guards(ob, on, "out")
+    check_guards(yb, yn, "dy")
+    check_guards(wb, wn, "dweights")
+
+
+@pytest.mark.parametrize("M,F,n", [(1, 32, None), (37, 96, None), (130, 160, 129), (300, 1376, 37), (64, 64, 0)])
+def test_swiglu_ckpt_writes_only_its_outputs(M, F, n):
+    u = dev(edge(M, 2 * F, M))
+    count = None if n is None else torch.tensor([n], dtype=torch.int32, device="cuda")
+    hb, hn, h = guarded_as(torch.bfloat16, M, F)
+    cb, cn, codes = guarded_as(torch.uint8, M, 2 * F)
+    sb, sf = guarded(bsq.bsq_sf_bytes(M, F // 16))
+    ab, _, amax = guarded_as(torch.float32, 4)
+    api.swiglu_ckpt(u, n_rows=count, out=(h, codes, sf, amax[:1]))
+    db, dn, du = guarded_as(torch.bfloat16, M, 2 * F)
+    gb, gn, again = guarded_as(torch.bfloat16, M, F)
+    api.swiglu_ckpt_bwd(h, codes, sf, n_rows=count, out=(du, again))
+    assert bsq.bsq_check() == bsq.BSQ_OK
+    rows = M if n is None else n
+    for buf, nbytes, what in ((hb, hn, "h"), (cb, cn, "codes"), (db, dn, "du"), (gb, gn, "h again")):
+        # the rows behind the count are as they were too
+        check_guards(buf, nbytes, what)
+        body = buf.cpu().numpy()[PAD:PAD + nbytes].reshape(M, -1)
+        assert (body[rows:] == CANARY).all(), f"{what}: rows that do not exist written"
+    check_sf(sb, M, F // 16, "checkpoint")
+    a = ab.cpu().numpy()
+    assert (a[:PAD] == CANARY).all() and (a[PAD + 4:] == CANARY).all(), "amax: bytes around it changed"

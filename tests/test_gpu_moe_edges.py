@@ -120,6 +120,77 @@ def test_swiglu_rows_that_do_not_exist_are_zeros_without_out(n):
         assert (du[n:].view(torch.int16) == 0).all() and (again[n:].view(torch.int16) == 0).all()
 
 
+# ------------------------------------------------------------------ router
+def check_route_large(z, k, mask, renorm, coef):
+    """As check_route of test_gpu_moe.py, with a reference that is vectorised over the tokens."""
+    T, E = z.shape
+    r = api.moe_route(dev(z), k, token_mask=None if mask is None else dev(mask), renorm=renorm, balance_coef=coef)
+    live = np.ones(T, bool) if mask is None else mask.numpy() != 0
+    zz = np.where(live[:, None], n64(z), -np.inf)
+    ids = np.argsort(-zz, axis=1, kind="stable")[:, :k]
+    top = np.take_along_axis(zz, ids, 1)
+    ids[~live] = -1
+    assert np.array_equal(ints(r.expert_ids), ids)
+    flat = np.where(ids < 0, E, ids).ravel()
+    order = np.argsort(flat, kind="stable")
+    n = int((ids >= 0).sum())
+    rows = np.full(T * k, -1)
+    rows[order[:n]] = np.arange(n)
+    assert np.array_equal(ints(r.rows).ravel(), rows)
+    index = np.full(T * k, order[0] // k)
+    index[:n] = order[:n] // k
+    assert np.array_equal(ints(r.row_index), index)
+    count = np.bincount(flat, minlength=E + 1)[:E]
+    assert np.array_equal(ints(r.counts), np.append(count, live.sum()))
+    assert np.array_equal(ints(r.row_offsets), np.append(0, np.cumsum(count)))
+    p = ref.softmax(zz, live)
+    w = ref.softmax(top, live) if renorm else np.where(live[:, None], np.take_along_axis(p, np.maximum(ids, 0), 1), 0)
+    rel = (3 * ref.spread(n64(z), live) + 4 + -(-E // 32) + 5 + 3) * U
+    within(n64(r.weights), w, rel * w + ref.TINY, "weights")
+    # the tokens of a warp, its warps, the chunks of a CTA, the CTAs, a tree
+    rel += (8 + 8 + 16 + T / 4096 + 16) * U
+    within(n64(r.prob_sums), p.sum(0), rel * p.sum(0) + T * ref.TINY, "prob_sums")
+    loss = coef * E * (count * p.sum(0)).sum() / k / live.sum() ** 2
+    within(n64(r.loss), [loss], (rel + (E / 32 + 20) * U) * loss, "loss")
+
+
+@pytest.mark.parametrize("T,E,k", [(25000, 160, 8), (25000, 256, 8), (21000, 140, 11), (20001, 600, 3),
+                                   (16384, 128, 8), (16000, 200, 2)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_route_with_several_chunks_per_cta(T, E, k, bf16):
+    """More chunks than CTAs (or than fit at once): masks are cleared and sums go on from chunk to chunk."""
+    mask = torch.ones(T, dtype=torch.uint8)
+    mask[5000:5400] = 0
+    mask[T - 70:T - 3] = 0
+    check_route_large(logits_of(T, E, T + E, bf16), k, mask, not bf16, 0.5)
+
+
+@pytest.mark.parametrize("T,E,k", [(60, 64, 10), (40, 20, 20), (30, 400, 20), (33, 300, 17), (50, 250, 32),
+                                   (70, 37, 9)])
+@pytest.mark.parametrize("bf16,renorm", [(False, True), (True, False), (True, True), (False, False)])
+def test_route_bwd_with_more_slots_than_lanes(T, E, k, bf16, renorm):
+    z = dev(logits_of(T, E, T * E, bf16, "shut" if E > 100 else "normal"))
+    r = api.moe_route(z, k, renorm=renorm)
+    a = torch.randn(T, k, generator=torch.Generator().manual_seed(k))
+    check_route_bwd(z, r, a, 1.5, 0.1, renorm)
+    check_route_bwd(z, r, a, None, 0.1, renorm)
+
+
+@pytest.mark.parametrize("T,E,k", [(30000, 32, 4), (30000, 31, 4), (30000, 24, 11), (25000, 160, 6), (25000, 158, 12),
+                                   (8000, 1000, 12), (8000, 999, 32)])
+@pytest.mark.parametrize("bf16,renorm", [(False, True), (True, False)])
+def test_route_bwd_of_more_tokens_than_fit_at_once(T, E, k, bf16, renorm):
+    """A group of lanes takes a second token: the row of shared memory between them is zero again."""
+    z = dev(logits_of(T, E, T + E, bf16))
+    mask = torch.ones(T, dtype=torch.uint8)
+    mask[100:400] = 0
+    mask[T - 500:T - 200] = 0
+    r = api.moe_route(z, k, token_mask=dev(mask), renorm=renorm)
+    a = torch.randn(T, k, generator=torch.Generator().manual_seed(k))
+    check_route_bwd(z, r, a, 1.5, 0.1, renorm)
+    check_route_bwd(z, r, a, None, 0.1, renorm)
+
+
 def exact_differences(T, E, seed):
     """fp32 logits whose differences from the largest are exact (multiples of 1/64 below 64 in magnitude), far apart:
     the weights' exponentials then have no rounding that grows with the distance."""
