@@ -639,7 +639,7 @@ int bsq_moe_combine(const void *y, int64_t R, int64_t H, int64_t ldy, const int3
     if (int st = device_state(&d)) return st;
     if (T == 0 || H == 0) return BSQ_OK;
     return bsq::launch_moe_combine(static_cast<const uint16_t *>(y), R, H, ldy, rows, weights, T, topk,
-                                   static_cast<uint16_t *>(out), ldo, d->num_sms, static_cast<cudaStream_t>(stream))
+                                   static_cast<uint16_t *>(out), ldo, static_cast<cudaStream_t>(stream))
                ? BSQ_ERR_CUDA
                : BSQ_OK;
 }
@@ -664,7 +664,7 @@ int bsq_moe_combine_bwd(const void *dout, int64_t ldo, const void *y, int64_t ld
     if (T == 0) return BSQ_OK;
     return bsq::launch_moe_combine_bwd(static_cast<const uint16_t *>(dout), ldo, static_cast<const uint16_t *>(y), ldy,
                                        y_codes, y_sf, R, H, rows, weights, T, topk, static_cast<uint16_t *>(dy), lddy,
-                                       dweights, d->num_sms, static_cast<cudaStream_t>(stream))
+                                       dweights, static_cast<cudaStream_t>(stream))
                ? BSQ_ERR_CUDA
                : BSQ_OK;
 }
@@ -689,7 +689,7 @@ int bsq_swiglu_ckpt(const void *u, int64_t M, int64_t F, int64_t ldu, const int3
     if (M == 0 || F == 0)
         return !amax || cudaMemsetAsync(amax, 0, sizeof(float), s) == cudaSuccess ? BSQ_OK : BSQ_ERR_CUDA;
     return bsq::launch_swiglu_ckpt(static_cast<const uint16_t *>(u), M, F, ldu, n_rows, static_cast<uint16_t *>(h),
-                                   ldh, codes, sf, reinterpret_cast<unsigned int *>(amax), d->num_sms, s)
+                                   ldh, codes, sf, reinterpret_cast<unsigned int *>(amax), s)
                ? BSQ_ERR_CUDA
                : BSQ_OK;
 }
@@ -706,7 +706,7 @@ int bsq_swiglu_ckpt_bwd(const void *dh, int64_t lddh, const uint8_t *codes, cons
     if (int st = device_state(&d)) return st;
     if (M == 0 || F == 0) return BSQ_OK;
     return bsq::launch_swiglu_ckpt_bwd(static_cast<const uint16_t *>(dh), lddh, codes, sf, M, F, n_rows,
-                                       static_cast<uint16_t *>(du), lddu, static_cast<uint16_t *>(h), ldh, d->num_sms,
+                                       static_cast<uint16_t *>(du), lddu, static_cast<uint16_t *>(h), ldh,
                                        static_cast<cudaStream_t>(stream))
                ? BSQ_ERR_CUDA
                : BSQ_OK;

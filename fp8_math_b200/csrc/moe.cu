@@ -1499,28 +1499,27 @@ __global__ void __launch_bounds__(kGlu, 1024 / kGlu)
     grid_dependency_wait();
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;  // even: a block's two lanes go together
-    uint32_t top = 0;
-    const int64_t round = (n + 31) & ~int64_t(31);  // the shuffle wants whole warps
-    for (int64_t i = (int64_t)blockIdx.x * kGlu + threadIdx.x; i < round; i += (int64_t)gridDim.x * kGlu) {
-        const uint32_t unit = i < n ? (uint32_t)i : 0u;
-        const uint32_t r = divide(unit, per);
-        const int64_t c = (int64_t)(unit - r * per.d) * 16;
-        uint32_t g[8], v[8], o[8];
-        load16(u + r * ldu + c, g);
-        load16(u + r * ldu + F + c, v);
-        uint32_t sg, sv;
-        const uint4 cg = mx_encode16(g, &sg), cv = mx_encode16(v, &sv);
-        if (i >= n) continue;
+    const int64_t i = (int64_t)blockIdx.x * kGlu + threadIdx.x;
+    if ((i & ~int64_t(31)) >= n) return;  // whole warps: the shuffles want all of their lanes
+    const uint32_t unit = i < n ? (uint32_t)i : 0u;
+    const uint32_t r = divide(unit, per);
+    const int64_t c = (int64_t)(unit - r * per.d) * 16;
+    uint32_t g[8], v[8], o[8], top = 0;
+    load16(u + r * ldu + c, g);
+    load16(u + r * ldu + F + c, v);
+    uint32_t sg, sv;
+    const uint4 cg = mx_encode16(g, &sg), cv = mx_encode16(v, &sv);
 #pragma unroll
-        for (int q = 0; q < 8; q++) {
-            const f32x2 gq = f2_pack(bf16_lo(g[q]), bf16_hi(g[q]));
-            f32x2 gs;
-            sigmoid2(gq, gs);
-            float a, b;
-            f2_unpack(f2_mul(gs, f2_pack(bf16_lo(v[q]), bf16_hi(v[q]))), a, b);
-            o[q] = pack_bf16(a, b);
-            top = max_bf16x2(top, o[q] & kAbs2);
-        }
+    for (int q = 0; q < 8; q++) {
+        const f32x2 gq = f2_pack(bf16_lo(g[q]), bf16_hi(g[q]));
+        f32x2 gs;
+        sigmoid2(gq, gs);
+        float a, b;
+        f2_unpack(f2_mul(gs, f2_pack(bf16_lo(v[q]), bf16_hi(v[q]))), a, b);
+        o[q] = pack_bf16(a, b);
+        top = max_bf16x2(top, o[q] & kAbs2);
+    }
+    if (i < n) {
         store16(h + r * ldh + c, o);
         uint8_t *row = codes + (int64_t)r * 2 * F + c;
         *reinterpret_cast<uint4 *>(row) = cg;
@@ -1549,46 +1548,46 @@ __global__ void __launch_bounds__(kGlu) swiglu_ckpt_bwd_kernel(const uint16_t *_
     grid_dependency_wait();
     const int64_t rows = n_rows ? min(M, (int64_t)max(__ldg(n_rows), 0)) : M;
     const int64_t n = rows * per.d;
-    for (int64_t i = (int64_t)blockIdx.x * kGlu + threadIdx.x; i < n; i += (int64_t)gridDim.x * kGlu) {
-        const uint32_t r = divide((uint32_t)i, per);
-        const int64_t c = (int64_t)((uint32_t)i - r * per.d) * 16;
-        const uint8_t *row = codes + (int64_t)r * 2 * F + c;
-        uint32_t d[8], x[8], y[8], w[8];
-        f32x2 g[8], v[8];
-        load16(dh + r * lddh + c, d);
-        const uint4 qg = __ldg(reinterpret_cast<const uint4 *>(row));
-        const uint4 qv = __ldg(reinterpret_cast<const uint4 *>(row + F));
-        const uint32_t sg = __ldg(sf + sf_offset(r, c >> 5, F >> 4));
-        const uint32_t sv = __ldg(sf + sf_offset(r, (c + F) >> 5, F >> 4));
-        e4m3x16(qg, g);
-        e4m3x16(qv, v);
-        const float fg = e8m0_value(sg), fv = e8m0_value(sv);
-        const f32x2 fg2 = f2_pack(fg, fg), fv2 = f2_pack(fv, fv);
+    const int64_t i = (int64_t)blockIdx.x * kGlu + threadIdx.x;
+    if (i >= n) return;
+    const uint32_t r = divide((uint32_t)i, per);
+    const int64_t c = (int64_t)((uint32_t)i - r * per.d) * 16;
+    const uint8_t *row = codes + (int64_t)r * 2 * F + c;
+    uint32_t d[8], x[8], y[8], w[8];
+    f32x2 g[8], v[8];
+    load16(dh + r * lddh + c, d);
+    const uint4 qg = __ldg(reinterpret_cast<const uint4 *>(row));
+    const uint4 qv = __ldg(reinterpret_cast<const uint4 *>(row + F));
+    const uint32_t sg = __ldg(sf + sf_offset(r, c >> 5, F >> 4));
+    const uint32_t sv = __ldg(sf + sf_offset(r, (c + F) >> 5, F >> 4));
+    e4m3x16(qg, g);
+    e4m3x16(qv, v);
+    const float fg = e8m0_value(sg), fv = e8m0_value(sv);
+    const f32x2 fg2 = f2_pack(fg, fg), fv2 = f2_pack(fv, fv);
 #pragma unroll
-        for (int q = 0; q < 8; q++) {
-            g[q] = f2_mul(g[q], fg2);
-            v[q] = f2_mul(v[q], fv2);
-        }
-#pragma unroll
-        for (int q = 0; q < 8; q++) {
-            f32x2 gs;
-            const f32x2 dd = f2_pack(bf16_lo(d[q]), bf16_hi(d[q])), sg2 = sigmoid2(g[q], gs);
-            float a, b;
-            f2_unpack(f2_mul(dd, gs), a, b);
-            y[q] = pack_bf16(a, b);
-            // s (1 + g (1 - s)) = s + gs (1 - s)
-            const f32x2 slope = f2_fma(gs, f2_sub(f2_pack(1.0f, 1.0f), sg2), sg2);
-            f2_unpack(f2_mul(f2_mul(dd, v[q]), slope), a, b);
-            x[q] = pack_bf16(a, b);
-            if (AGAIN) {
-                f2_unpack(f2_mul(gs, v[q]), a, b);
-                w[q] = pack_bf16(a, b);
-            }
-        }
-        store16(du + r * lddu + c, x);
-        store16(du + r * lddu + F + c, y);
-        if (AGAIN) store16(h + r * ldh + c, w);
+    for (int q = 0; q < 8; q++) {
+        g[q] = f2_mul(g[q], fg2);
+        v[q] = f2_mul(v[q], fv2);
     }
+#pragma unroll
+    for (int q = 0; q < 8; q++) {
+        f32x2 gs;
+        const f32x2 dd = f2_pack(bf16_lo(d[q]), bf16_hi(d[q])), sg2 = sigmoid2(g[q], gs);
+        float a, b;
+        f2_unpack(f2_mul(dd, gs), a, b);
+        y[q] = pack_bf16(a, b);
+        // s (1 + g (1 - s)) = s + gs (1 - s)
+        const f32x2 slope = f2_fma(gs, f2_sub(f2_pack(1.0f, 1.0f), sg2), sg2);
+        f2_unpack(f2_mul(f2_mul(dd, v[q]), slope), a, b);
+        x[q] = pack_bf16(a, b);
+        if (AGAIN) {
+            f2_unpack(f2_mul(gs, v[q]), a, b);
+            w[q] = pack_bf16(a, b);
+        }
+    }
+    store16(du + r * lddu + c, x);
+    store16(du + r * lddu + F + c, y);
+    if (AGAIN) store16(h + r * ldh + c, w);
 }
 
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
@@ -1761,7 +1760,7 @@ int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s) {
 }
 
 int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
-                       int64_t T, int topk, uint16_t *out, int64_t ldo, int, cudaStream_t s) {
+                       int64_t T, int topk, uint16_t *out, int64_t ldo, cudaStream_t s) {
     auto run = [&](auto kern) {
         return launch_dependent(kern, dim3((unsigned)T, (unsigned)((H + 1023) / 1024)), dim3(128), 0, s, y, R, H, ldy,
                                 rows, weights, topk, out, ldo) != cudaSuccess;
@@ -1771,7 +1770,7 @@ int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, con
 
 int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y, int64_t ldy, const uint8_t *codes,
                            const uint8_t *sf, int64_t R, int64_t H, const int32_t *rows, const float *weights,
-                           int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, int, cudaStream_t s) {
+                           int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, cudaStream_t s) {
     const uint32_t slots = (uint32_t)(T * topk);
     auto run = [&](auto kern) {
         return launch_dependent(kern, dim3((slots + 3) / 4), dim3(128), 0, s, dout, ldo, y, ldy, codes, sf, R, H, rows,
@@ -1781,7 +1780,7 @@ int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y,
 }
 
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
-                       int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int, cudaStream_t s) {
+                       int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, cudaStream_t s) {
     const unsigned grid = (unsigned)((M * (F / 16) + kGlu - 1) / kGlu);
     const UnitDiv per = unit_div((uint32_t)(F / 16));
     if (amax && launch_dependent(zero_word_kernel, dim3(1), dim3(1), 0, s, amax) != cudaSuccess) return 1;
@@ -1791,7 +1790,7 @@ int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, con
 
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
                            int64_t F, const int32_t *n_rows, uint16_t *du, int64_t lddu, uint16_t *h, int64_t ldh,
-                           int num_sms, cudaStream_t s) {
+                           cudaStream_t s) {
     const unsigned grid = (unsigned)((M * (F / 16) + kGlu - 1) / kGlu);
     const UnitDiv per = unit_div((uint32_t)(F / 16));
     auto run = [&](auto kern) {

@@ -49,18 +49,17 @@ struct RouteBwdArgs {
 int launch_moe_route_bwd(const RouteBwdArgs &a, int num_sms, cudaStream_t s);
 
 int launch_moe_combine(const uint16_t *y, int64_t R, int64_t H, int64_t ldy, const int32_t *rows, const float *weights,
-                       int64_t T, int topk, uint16_t *out, int64_t ldo, int num_sms, cudaStream_t s);
+                       int64_t T, int topk, uint16_t *out, int64_t ldo, cudaStream_t s);
 // y as bf16, or (y NULL) as MXFP8 codes with swizzled scales.
 int launch_moe_combine_bwd(const uint16_t *dout, int64_t ldo, const uint16_t *y, int64_t ldy, const uint8_t *codes,
                            const uint8_t *sf, int64_t R, int64_t H, const int32_t *rows, const float *weights,
-                           int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, int num_sms,
-                           cudaStream_t s);
+                           int64_t T, int topk, uint16_t *dy, int64_t lddy, float *dweights, cudaStream_t s);
 
 // amax may be NULL.
 int launch_swiglu_ckpt(const uint16_t *u, int64_t M, int64_t F, int64_t ldu, const int32_t *n_rows, uint16_t *h,
-                       int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, int num_sms, cudaStream_t s);
+                       int64_t ldh, uint8_t *codes, uint8_t *sf, unsigned int *amax, cudaStream_t s);
 int launch_swiglu_ckpt_bwd(const uint16_t *dh, int64_t lddh, const uint8_t *codes, const uint8_t *sf, int64_t M,
                            int64_t F, const int32_t *n_rows, uint16_t *du, int64_t lddu, uint16_t *h, int64_t ldh,
-                           int num_sms, cudaStream_t s);
+                           cudaStream_t s);
 
 }  // namespace bsq
