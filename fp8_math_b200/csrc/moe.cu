@@ -313,9 +313,9 @@ struct Candidates<float, LPT, Q> {
 // For k <= L: a sorted list of the token's L best, built without a branch: a
 // lane sorts its logits by networks of maxima and minima, and log2(LPT)
 // exchanges merge the lanes' lists (the larger of a[i] and b[L-1-i] are the L
-// best of two sorted lists, in bitonic order).  Against rounds of one maximum
-// each this took the whole call from 96 to 81 us at 131072x256, k = 8, and from
-// 5.7 to 4.3 us at 64x64.  The entries are logits with the expert in their low bits, as above.
+// best of two sorted lists, in bitonic order).  The whole call at 131072x256,
+// k = 8: 63 us, with rounds of one maximum each 92; at 64x64 4.4 and 6.2.  The
+// entries are logits with the expert in their low bits, as above.
 // An fp32 logit gives its lowest ceil(log2 E) bits for it; where two such
 // truncated logits meet in the list or at its end, the order is not certain and
 // the warp's tokens go through the rounds instead.  NaN entries (-inf logits)
@@ -407,8 +407,8 @@ BSQ_DEV void best_list(const Row<In, LPT, Q> &row, int sub, uint32_t bits, float
 // maxima hold the L best logits (a quad before which L others come has L
 // logits before each of its own), so lists of quads come first, then lane i
 // reads quad i's four logits again, and lists are made of those.  Five and
-// more quads a lane: 131072x256, k = 8, then takes 71 us instead of 77.  The
-// list is that of the lanes sub < L alone.
+// more quads a lane: the call takes 63 us instead of 73 at 131072x256, k = 8, 53
+// instead of 55 at 131072x160.  The list is that of the lanes sub < L alone.
 template <int L, typename In, int LPT, int Q>
 BSQ_DEV void best_of_quads(const Row<In, LPT, Q> &row, const In *logits, int sub, int E, bool vec, uint32_t bits,
                            float v[L]) {
@@ -537,8 +537,8 @@ struct RouteOut {
 
 // The rest of the call by the CTAs of one cluster, 64 tokens each: every one adds
 // up all masks' counts, those of the CTAs before it apart, and places its slots.
-// Against a second launch: 512x128, k = 8, 7.1 us on the device instead of 8.3, and
-// a launch's host time less.
+// Against a second launch: 512x128, k = 8, 7.2 us on the device instead of 8.4 (with
+// 1000 experts 25.7 and 25.5), and a launch's host time less.
 BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, const uint16_t *sel, const float *sel_x,
                           const float *inv, int64_t T, UnitDiv kd, int E, int ctas, int want_p, const RouteOut &out,
                           float coef) {
@@ -616,7 +616,8 @@ BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, c
 }
 
 // Pass 1.  A CTA takes chunks of kChunk consecutive tokens in turn, LPT lanes a
-// token; the sums of probabilities stay in its registers.  The softmax sum runs
+// token; the sums of probabilities stay in its registers (with 32 fp32 logits a
+// lane, 193 to 256 and 385 experts and more, some spill).  The softmax sum runs
 // over the same registers as the choice.  The chosen experts go into one 64-bit
 // mask of tokens per expert, whose population count is the chunk's count and
 // whose bits below a token are that token's rank in the chunk: the order "by
@@ -624,12 +625,13 @@ BSQ_DEV void finish_route(unsigned long long *masks, float *red, int32_t *off, c
 // with at least one expert.  With `ctas` > 0 the chunks are one cluster, a CTA
 // each, which finishes the call (rows, offsets, loss) from one another's masks and
 // sums in shared memory.  L: k <= L by sorted lists; 0: rounds for any k.
-// 131072x256, k = 8: three quarters of the call's 61 us, bound by instructions (235
-// per token; minima and maxima run at half rate).
+// 131072x256, k = 8: three quarters of the call's 63 us.  261 instructions a token; a
+// third of the issue slots stay empty, with three CTAs (24 warps) on an SM.
 // (The launch bound is there for the registers: 64 where a lane has few logits, so
 // that two CTAs of 512 threads share an SM, else 80.)
 template <typename In, int LPT, int Q, int L>
-__global__ void __launch_bounds__(Q <= 2 ? 1024 : 768) route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
+__global__ void __launch_bounds__(Q <= 2 ? 1024 : 768)
+    route_topk_kernel(const In *__restrict__ logits, int64_t T, int E, int64_t ldl,
                                                          int vec, const uint8_t *__restrict__ mask, UnitDiv kd,
                                                          int renorm, int want_p, int ctas, RouteOut out, int64_t nchunk,
                                                          uint8_t *__restrict__ hist, float *__restrict__ psum,
@@ -880,8 +882,6 @@ BSQ_DEV void cta_scan(const int32_t *n, int E, int32_t *off, int *wsum) {
 // before + the chunk's prefix in its block + the rank inside the chunk; the
 // rows past the last routed one repeat the first row's token.  A CTA takes
 // `span` chunks of one block; one more writes the offsets and the loss.
-// (Laying the rows out by expert in shared memory, to write row_index in runs,
-// took 12 us more than the scattered writes at 131072x8 slots.)
 __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd, int E, int64_t nchunk, int span,
                                                           const uint8_t *__restrict__ hist,
                                                           const uint16_t *__restrict__ prefix,
@@ -978,7 +978,10 @@ __global__ void __launch_bounds__(256) route_place_kernel(int64_t T, UnitDiv kd,
 // apart, which gives the experts' offsets and its own prefix, and places its
 // slots.  Three bytes are added before they are widened (64 a chunk), and two
 // counts share a 32-bit sum (512 chunks at most).  One more CTA writes the
-// offsets, the sums of the probabilities and the loss.
+// offsets, the sums of the probabilities and the loss.  The whole call against
+// passes 2 and 3 apart: 8.7 and 9.3 us at 2048x128 (4 KB of counts), 13.6 and 13.9
+// at 16384x64 (17 KB); nearer the limit the passes apart are the faster ones, 15.1
+// and 12.9 at 16384x96 (26 KB), 24.5 and 16.0 at 16384x160 (42 KB).
 constexpr int kSmallHist = 48 * 1024, kSmallChunks = 512;
 
 __global__ void __launch_bounds__(256) route_scan_place_kernel(int64_t T, UnitDiv kd, int E, int nchunk,
@@ -1127,7 +1130,9 @@ BSQ_DEV void store_row(uint16_t *to, const float *row, int E, int sub) {
 
 // CTAs per SM, and the grid is no larger: five at 48 registers where a lane's
 // logits leave that many free, six where the softmax is not needed (shared
-// memory).  131072x256 takes 50 us with eight CTAs per SM in turns, 35 with three.
+// memory).  With eight CTAs per SM in turns, 131072x256 takes 37 us instead of 34
+// and 100003x160 19.9 instead of 18.7 (bf16; fp32 logits at 131072x256 48 instead
+// of 53).
 template <int Q, bool NEED_P>
 constexpr int bwd_ctas() {
     return !NEED_P ? 6 : Q <= 5 ? 5 : 3;
@@ -1283,7 +1288,8 @@ __global__ void __launch_bounds__(256, bwd_ctas<Q, NEED_P>())
 // ------------------------------------------------------------------ combine
 // out[t] = sum_j w_tj y[rows_tj]: a CTA of 128 threads takes 1024 columns of
 // one token, each thread eight of them over all k rows.  Memory bound:
-// 16384x8x4096 takes 185 us, the measured copy rate (199 us with one row in flight).
+// 16384x8x4096 takes 185 us, the measured copy rate.  B rows in flight: with one it
+// takes 201 us; k = 2 with B = 4, half of them empty, 76 us at 16384x2x4096 instead of 70.
 template <int B>
 __global__ void __launch_bounds__(128) combine_kernel(const uint16_t *__restrict__ y, int64_t R, int64_t H, int64_t ldy,
                                                       const int32_t *__restrict__ rows,
@@ -1362,10 +1368,8 @@ BSQ_DEV void bwd8(uint4 dq, const f32x2 v[4], f32x2 w2, f32x2 &dot2, uint16_t *t
 // slot, so that empty slots cost nothing and no sum leaves the warp; a
 // token's dout is read from DRAM by one of its warps and by the others from
 // L1.  Memory bound: y read once, dy written once.  16384x8x4096: 351 us, the
-// measured copy rate, against 410 with one CTA per token (354 with eight warps a
-// CTA instead of four); from 8-bit rows 315 us, bound by the writes (a fill
-// reaches 3.9 TB/s).  Warps that stay and take slot after slot were slower (420
-// us): the order of the rows in flight spreads.
+// measured copy rate (354 with eight warps a CTA instead of four); from 8-bit rows
+// 310 us (321).
 template <bool MX>
 __global__ void __launch_bounds__(128) combine_bwd_kernel(const uint16_t *__restrict__ dout, int64_t ldo,
                                                           const uint16_t *__restrict__ y, int64_t ldy,
@@ -1484,13 +1488,12 @@ __global__ void zero_word_kernel(unsigned int *p) {
     *p = 0;
 }
 
-constexpr int kGlu = 128;  // threads of a gated SiLU CTA; 256: forward 135 us instead of 131
+// Threads of a gated SiLU CTA; with 256, 131072x768 takes 129 us instead of 127, its backward 156 instead of 149.
+constexpr int kGlu = 128;
 
 // Memory bound: 8.06 bytes per h.  A thread takes 16 columns of the gate and
 // the same 16 of v (64 bytes in flight), so two lanes share a block of 32 and
-// write one scale byte each.  131072x768: 131 us, 95 % of the measured copy
-// rate; 8 columns a thread took 172 us (twice the addresses and exchanges), and
-// a grid that stays resident no less.
+// write one scale byte each.  131072x768: 127 us, 98 % of the measured copy rate.
 __global__ void __launch_bounds__(kGlu, 1024 / kGlu)
     swiglu_ckpt_kernel(const uint16_t *__restrict__ u, int64_t M, int64_t F, int64_t ldu, UnitDiv per,
                        const int32_t *__restrict__ n_rows, uint16_t *__restrict__ h, int64_t ldh,
@@ -1536,7 +1539,7 @@ __global__ void __launch_bounds__(kGlu, 1024 / kGlu)
 
 // From the checkpoint's g and v: du = (dh v s (1 + g (1 - s)), dh g s), and,
 // when h is wanted, h = g s v again.  Memory bound: 8.06 bytes per element of
-// dh, 10.06 with h.
+// dh, 10.06 with h (131072x768: 118 and 149 us).
 template <bool AGAIN>
 __global__ void __launch_bounds__(kGlu) swiglu_ckpt_bwd_kernel(const uint16_t *__restrict__ dh, int64_t lddh,
                                                               const uint8_t *__restrict__ codes,
@@ -1600,7 +1603,11 @@ bool quads(const void *p, int64_t E, int64_t ld) {
 
 // f.template operator()<LPT, Q>() with LPT lanes per token, Q quads of logits per
 // lane.  Eight lanes per token wherever 32 logits per lane are enough: a round
-// of the choice serves four tokens of a warp.
+// of the choice serves four tokens of a warp.  Against the next larger step the
+// ones at 96, 160, 192 and 384 take 131072 tokens, k = 8, from 50 to 45, 60 to 54,
+// 61 to 56 and 105 to 98 us (bf16; fp32 57 to 53, 80 to 65, 82 to 70, 135 to 117), the
+// gradient from 20 to 18, 31 to 24, 33 to 29 and 58 to 51 (fp32 22 to 21, 35 both,
+// 38 both, 70 to 76).
 template <class F>
 int by_experts(int64_t E, F f) {
     if (E <= 32) return f.template operator()<8, 1>();
@@ -1619,10 +1626,17 @@ bool small_hist(int64_t nchunk, int E) {
     return E <= 256 && nchunk <= kSmallChunks && nchunk * hist_row(E) <= kSmallHist;
 }
 
-// First pass: 16 warps take a chunk in half as many turns, while all chunks fit
-// on the SMs at once; else 8 warps.  Many experts: two chunks a CTA, so that the
-// sums of probabilities leave the registers half as often (more leaves the last
-// CTAs alone: 131072x256 takes 67 us with as many CTAs as fit, 64 with this).
+// First pass: 16 warps take a chunk in half as many turns as 8, up to two chunks
+// an SM.  Up to 64 experts both chunks fit on it at once (64 registers); with
+// more experts the second waits for the first, and 16 warps are the faster all
+// the same.  The call with 16 and 8 warps, k = 8: 11.4 and 16.0 us at 16384x64,
+// 19.6 and 20.6 at 16384x128, 18.3 and 22.1 at 16384x256, 47 and 90 at
+// 16384x1000 (bf16; fp32 alike); 8 warps win a few sizes of 96 to 160 experts, by
+// 13 % at most (12000x160: 20.9 and 18.2).
+// Many experts and more chunks: two chunks a CTA, so that the sums of
+// probabilities leave the registers half as often: 131072x256 takes 63.4 us, 64.5
+// with a chunk a CTA, 66.5 with as many CTAs as fit at once (40000x256: 30.3, 27.6
+// and 30.6).
 int topk_threads(int64_t nchunk, int num_sms) { return nchunk <= 2 * num_sms ? 512 : 256; }
 int64_t topk_grid(int64_t nchunk, int64_t E, int num_sms) {
     return E > 128 && topk_threads(nchunk, num_sms) == 256 ? (nchunk + 1) / 2 : nchunk;

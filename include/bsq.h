@@ -402,7 +402,7 @@ BSQ_API int bsq_grouped_gemm_nvfp4_out(int fmt, int G, const int32_t *row_offset
  * section "A precision choice for each stage": expert layers in NVFP4
  * forward, MXFP8 backward) and not these operators; their definitions
  * follow here.  All of them sum in fp32 in a fixed order: the same inputs
- * give the same bits.
+ * give the same bits.  No output may overlap an input or another output.
  *
  * Slots.  Each token has topk slots; slot j of token t holds an expert, the
  * routed row the token has there, and a weight.  A slot is empty when the
@@ -497,8 +497,9 @@ BSQ_API int bsq_swiglu_ckpt(const void *u_bf16, int64_t M, int64_t F, int64_t ld
 /* Its gradient from the checkpoint (g and v are the decoded MXFP8 values) and
  * dh [M][F] (bf16), with s = sigmoid(g): du [M][2F] (bf16) holds
  * dh * v * s * (1 + g * (1 - s)) and dh * g * s.  h_bf16_dev, if not NULL,
- * also receives h formed again from the checkpoint, for the weight gradient
- * of the product that consumed it.  n_rows_dev as above. */
+ * also receives h formed again from the checkpoint, for a caller that forms
+ * the weight gradient of the product that consumed it (this library has no
+ * grouped product over tokens).  n_rows_dev as above. */
 BSQ_API int bsq_swiglu_ckpt_bwd(const void *dh_bf16, int64_t lddh, const uint8_t *codes_dev, const uint8_t *sf_dev,
                                 int64_t M, int64_t F, const int32_t *n_rows_dev, void *du_bf16_dev, int64_t lddu,
                                 void *h_bf16_dev, int64_t ldh, void *stream);
